@@ -19,7 +19,9 @@
  * conventions: tp_mlp_allreduce_residual_rmsnorm (the all-reduce of the
  * ranks' partials fused with the residual add and RMSNorm that follow it) and
  * tp_mlp_merge_attention_partials (decode context parallelism's merge of the
- * KV shards' partial attention results).  Their declarations are at the end.
+ * KV shards' partial attention results).  A paged key/value cache in 8 bits
+ * (tp_mlp_kv8_*) holds a rank's part of the history, and its attention
+ * produces those partial results.  Their declarations are at the end.
  *
  * Conventions for every entry point
  *   - Matrices are row-major and densely packed (row stride = row length).
@@ -506,6 +508,192 @@ int tp_mlp_ipc_close_handle(void *dev_ptr, size_t offset);
  * stream's work up to this call has completed.
  */
 int tp_mlp_copy_async(void *dst, const void *src, size_t bytes, tp_mlp_stream_t stream);
+
+/*
+ * ---- Paged key/value cache in 8 bits ----------------------------------------
+ *
+ * What produces the partial results that tp_mlp_merge_attention_partials
+ * merges: a rank's part of the KV history ("LLM 推理并行化：先找瓶颈，再决定
+ * 怎么切", §三 4)) held as e4m3 codes in pages of page_size tokens, with one
+ * fp32 scale for each page (block of tokens) and KV head, for keys and values
+ * apart.  The pages give no storage format, quantisation or page handling;
+ * those are this library's own.
+ *
+ *   value = e4m3(code) * scale[layer][page][kv_head]
+ *
+ * A scale that the library writes is a power of two: for rows whose largest
+ * finite magnitude is amax it is 2^ceil(log2(amax / 448)), at least 2^-100
+ * (448 is e4m3's largest number).  Dividing by it is exact, so a code is the
+ * value's nearest e4m3 number (ties to even); infinities become +-448, NaN
+ * stays NaN.
+ *
+ * Every buffer is the caller's device memory.  All layers share one page map:
+ * sequence s holds lengths[s] tokens, token t in slot t % page_size of page
+ * table[s][t / page_size].  A page may belong to several sequences (refcount).
+ * A page with refcount 0 is free.  A page's slots behind its sequence's end
+ * hold anything.
+ *
+ * Device-side checks: what the host cannot see (sequence numbers, lengths,
+ * page numbers) the kernels check before they use it; what does not fit is
+ * left out, nothing outside the buffers is touched, and a bit of *status is
+ * set (tp_mlp_kv8_get_status).  A sequence number of -1 marks an unused entry
+ * of a list (a padded batch) and is passed over without a flag.
+ */
+typedef struct {
+    void *k, *v;               /* e4m3, layers x num_pages x kv_heads x page_size x head_dim */
+    float *k_scale, *v_scale;  /* layers x num_pages x kv_heads, positive                    */
+    int *table;                /* max_seqs x max_pages page numbers; -1 = none               */
+    int *lengths;              /* max_seqs                                                   */
+    int *refcount;             /* num_pages: the sequences that hold the page                */
+    int *status;               /* one word, zero at the start                                */
+    int layers, num_pages;
+    int kv_heads;              /* 1..256                                                     */
+    int page_size;             /* 16, 32, 64, 128 or 256                                     */
+    int head_dim;              /* 64, 128 or 256                                             */
+    int max_seqs, max_pages;   /* rows of the table, pages a sequence can hold               */
+} tp_mlp_kv8_cache;
+
+/* Bits of the status word. */
+typedef enum {
+    TP_MLP_KV8_BAD_SEQUENCE = 1, /* a sequence number outside the table, or given twice to a
+                                    call that changes it (the first entry counts)           */
+    TP_MLP_KV8_BAD_LENGTH = 2,   /* a length or token count below zero, beyond the table's
+                                    room or at odds with the call                           */
+    TP_MLP_KV8_BAD_PAGE = 4,     /* a page number outside the pool                           */
+    TP_MLP_KV8_NO_PAGES = 8,     /* too few free pages: the whole tp_mlp_kv8_reserve call
+                                    changed nothing                                          */
+    TP_MLP_KV8_SHARED_PAGE = 16  /* an append met a page that other sequences hold too       */
+} tp_mlp_kv8_flag;
+
+/* Most sequences (or page pairs) in one call's list. */
+#define TP_MLP_KV8_MAX_LIST 1024
+
+/*
+ * Status of the cache's calls so far: synchronises the device, stores the
+ * status word's bits in *flags and clears it.  TP_MLP_OK also when bits are set.
+ */
+int tp_mlp_kv8_get_status(const tp_mlp_kv8_cache *cache, int *flags);
+
+/* Device workspace (bytes) of tp_mlp_kv8_reserve and tp_mlp_kv8_compact; 0 for
+ * an invalid cache.  No contents are kept between calls. */
+size_t tp_mlp_kv8_pages_workspace_bytes(const tp_mlp_kv8_cache *cache);
+
+/*
+ * Make room for counts[i] more tokens in sequence seqs[i] and count them in
+ * its length, for n sequences.  New pages are the lowest-numbered free ones,
+ * given out in the list's order (refcount 1).  If a sequence's next token
+ * falls into a page that is already partly filled and that other sequences
+ * hold too, that page's contents are first copied, in every layer, to a new
+ * page of the sequence's own, taken before its other new pages; where all
+ * holders of such a page are in the list, the first of them keeps it and only
+ * the others copy.  The call serves all its valid entries, or, with too few
+ * free pages, none of them (TP_MLP_KV8_NO_PAGES).
+ *   seqs, counts  device, n ints each (counts >= 0; seqs NULL: sequence i)
+ *   workspace     device, tp_mlp_kv8_pages_workspace_bytes bytes
+ * n <= TP_MLP_KV8_MAX_LIST (TP_MLP_ERR_SHAPE).  n == 0 is a no-op.
+ */
+int tp_mlp_kv8_reserve(const tp_mlp_kv8_cache *cache, const int *seqs, const int *counts, int n,
+                       void *workspace, size_t workspace_bytes, tp_mlp_stream_t stream);
+
+/*
+ * children[i] becomes a copy of parents[i] that shares its pages (refcounts
+ * go up, no contents move; tp_mlp_kv8_reserve copies a shared page when it is
+ * written to).  A child must be empty (length 0), may be in the list once, and
+ * may not be a parent in the same list; a pair that breaks this is left out
+ * and flagged.  Both lists: device, n ints, n <= TP_MLP_KV8_MAX_LIST.
+ */
+int tp_mlp_kv8_fork(const tp_mlp_kv8_cache *cache, const int *parents, const int *children, int n,
+                    tp_mlp_stream_t stream);
+
+/*
+ * Cut sequence seqs[i] to new_lengths[i] tokens (NULL: to none, which frees
+ * it).  Pages behind the new end are given up: their table entries become -1,
+ * their refcounts go down.  A new length above the old one is flagged and
+ * changes nothing.  Lists: device, n ints, n <= TP_MLP_KV8_MAX_LIST.
+ */
+int tp_mlp_kv8_truncate(const tp_mlp_kv8_cache *cache, const int *seqs, const int *new_lengths, int n,
+                        tp_mlp_stream_t stream);
+
+/*
+ * Copy whole pages, in every layer (codes and scales): page pairs[2*i] to page
+ * pairs[2*i + 1].  Table and refcounts stay.  A pair with a negative page is
+ * passed over; a pair whose destination is also a source, or an earlier
+ * pair's destination, is left out and flagged (TP_MLP_KV8_BAD_PAGE), except
+ * that a page copied to itself is passed over.
+ *   pairs  device, 2 * n ints, n <= TP_MLP_KV8_MAX_LIST
+ */
+int tp_mlp_kv8_copy_pages(const tp_mlp_kv8_cache *cache, const int *pairs, int n, tp_mlp_stream_t stream);
+
+/*
+ * Bring the pages in use to the front of the pool: with L pages in use, those
+ * numbered L and above move, in order, to the free pages below L, in order, in
+ * every layer; table and refcounts follow.  new_index (device, num_pages ints,
+ * or NULL) receives where each page's contents are afterwards (-1 for a page
+ * that was free).  The moved pages' old places are free and keep their bytes.
+ *   workspace  device, tp_mlp_kv8_pages_workspace_bytes bytes
+ */
+int tp_mlp_kv8_compact(const tp_mlp_kv8_cache *cache, int *new_index, void *workspace, size_t workspace_bytes,
+                       tp_mlp_stream_t stream);
+
+/*
+ * Quantise new keys and values of one layer into the pages.  Sequence seqs[i]
+ * takes the input rows cu_tokens[i] .. cu_tokens[i + 1] - 1 (cu_tokens NULL:
+ * tokens / n rows each) as its LAST tokens: call it after tp_mlp_kv8_reserve
+ * has counted them.  The other tokens of a page that was partly filled keep
+ * their values; if the new rows need a larger scale, the page's codes are
+ * brought to it (exact but for codes that become e4m3 subnormals).  A page
+ * whose first slot is written takes its scale from the new rows alone.
+ *   layer      0 <= layer < layers
+ *   k, v       device, `tokens` rows of kv_heads x head_dim elements of `dtype`,
+ *              a row every row_stride elements (>= kv_heads * head_dim; a row
+ *              starts on a 16-byte boundary)
+ *   seqs       device, n ints (NULL: sequence i); each sequence once
+ *   cu_tokens  device, n + 1 ints, ascending from 0, or NULL
+ * n <= TP_MLP_KV8_MAX_LIST, tokens <= 4194304; without cu_tokens, tokens % n
+ * == 0 (TP_MLP_ERR_SHAPE).  tokens == 0 or n == 0 is a no-op.
+ */
+int tp_mlp_kv8_append(const tp_mlp_kv8_cache *cache, int layer, const void *k, const void *v, long long row_stride,
+                      int tokens, const int *seqs, const int *cu_tokens, int n, int dtype, tp_mlp_stream_t stream);
+
+/*
+ * Attention of q_len queries of each of n sequences over one layer's cache.
+ * Query j of entry i stands at position p = positions[i] + j, counted from the
+ * cache's first token of that sequence, and sees the tokens t <= p with
+ * t < length; positions NULL: the sequence's last q_len places.  (A rank that
+ * holds a later part of the history passes positions counted from its own
+ * first token; below zero, nothing is seen.)  With heads / kv_heads = g, query
+ * heads h*g .. h*g + g - 1 use KV head h:
+ *     s_t = scale * q . k_t,   out = sum_t exp(s_t) v_t / sum_t exp(s_t)
+ * A query that sees no token gets zeros.  Entries whose sequence number is -1
+ * or invalid leave their rows of the output as they were; keys of an invalid
+ * page count as unseen.  fp32 softmax and accumulation.
+ *   q          device, n * q_len rows of heads x head_dim elements of `dtype`,
+ *              a row every row_stride elements (16-byte row starts)
+ *   out        device, n x q_len x heads x head_dim of `dtype`, dense
+ *   seqs       device, n ints (NULL: sequence i); a sequence may occur again
+ *   positions  device, n ints, or NULL
+ *   workspace  device, tp_mlp_kv8_attention_workspace_bytes bytes; no contents
+ *              are kept between calls, but calls that overlap need their own
+ * 1 <= n <= TP_MLP_KV8_MAX_LIST (0 is a no-op), 1 <= q_len <= 128, heads a
+ * multiple of kv_heads with heads / kv_heads <= 128, scale finite.
+ */
+size_t tp_mlp_kv8_attention_workspace_bytes(const tp_mlp_kv8_cache *cache, int n, int q_len, int heads);
+int tp_mlp_kv8_attention(const tp_mlp_kv8_cache *cache, int layer, const void *q, long long row_stride,
+                         const int *seqs, const int *positions, int n, int q_len, int heads, float scale, int dtype,
+                         void *out, void *workspace, size_t workspace_bytes, tp_mlp_stream_t stream);
+
+/*
+ * The same attention left as one rank's partial result, in the form that
+ * tp_mlp_merge_attention_partials takes (rows = n * q_len * heads): the
+ * maximum score, the sum of exp(score - maximum) and the exp-weighted sum of
+ * the values of every query row; -inf, 0 and zeros for a row that sees no
+ * token.  maximum and exp_sum: device fp32, `rows` each; weighted: device,
+ * rows x head_dim of `dtype`.  Everything else as tp_mlp_kv8_attention.
+ */
+int tp_mlp_kv8_attention_partials(const tp_mlp_kv8_cache *cache, int layer, const void *q, long long row_stride,
+                                  const int *seqs, const int *positions, int n, int q_len, int heads, float scale,
+                                  int dtype, float *maximum, float *exp_sum, void *weighted, void *workspace,
+                                  size_t workspace_bytes, tp_mlp_stream_t stream);
 
 /* Human-readable name of a status code (static string; no counterpart in the pages). */
 const char *tp_mlp_status_string(int status);

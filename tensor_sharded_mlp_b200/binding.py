@@ -37,6 +37,18 @@ _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _vpp = ctypes.POINTER(ctypes.c_void_p)
 
+
+class Kv8Cache(ctypes.Structure):
+    """tp_mlp_kv8_cache: the paged 8-bit key/value cache's buffers and sizes."""
+    _fields_ = [(_n, _vp) for _n in ("k", "v", "k_scale", "v_scale", "table", "lengths", "refcount", "status")] + \
+               [(_n, _i) for _n in ("layers", "num_pages", "kv_heads", "page_size", "head_dim", "max_seqs", "max_pages")]
+
+
+_kv8 = ctypes.POINTER(Kv8Cache)
+_ll = ctypes.c_longlong
+KV8_MAX_LIST = 1024
+KV8_FLAGS = {1: "BAD_SEQUENCE", 2: "BAD_LENGTH", 4: "BAD_PAGE", 8: "NO_PAGES", 16: "SHARED_PAGE"}
+
 _SIGS = {
     "tp_mlp_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i, _i, _i, _i]),
     "tp_mlp_destroy": (_i, [_vp]),
@@ -67,6 +79,18 @@ _SIGS = {
     "tp_mlp_ipc_open_handle": (_i, [_vp, _sz, ctypes.POINTER(_vp)]),
     "tp_mlp_ipc_close_handle": (_i, [_vp, _sz]),
     "tp_mlp_copy_async": (_i, [_vp, _vp, _sz, _vp]),
+    "tp_mlp_kv8_get_status": (_i, [_kv8, ctypes.POINTER(_i)]),
+    "tp_mlp_kv8_pages_workspace_bytes": (_sz, [_kv8]),
+    "tp_mlp_kv8_reserve": (_i, [_kv8, _vp, _vp, _i, _vp, _sz, _vp]),
+    "tp_mlp_kv8_fork": (_i, [_kv8, _vp, _vp, _i, _vp]),
+    "tp_mlp_kv8_truncate": (_i, [_kv8, _vp, _vp, _i, _vp]),
+    "tp_mlp_kv8_copy_pages": (_i, [_kv8, _vp, _i, _vp]),
+    "tp_mlp_kv8_compact": (_i, [_kv8, _vp, _vp, _sz, _vp]),
+    "tp_mlp_kv8_append": (_i, [_kv8, _i, _vp, _vp, _ll, _i, _vp, _vp, _i, _i, _vp]),
+    "tp_mlp_kv8_attention_workspace_bytes": (_sz, [_kv8, _i, _i, _i]),
+    "tp_mlp_kv8_attention": (_i, [_kv8, _i, _vp, _ll, _vp, _vp, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _sz, _vp]),
+    "tp_mlp_kv8_attention_partials": (_i, [_kv8, _i, _vp, _ll, _vp, _vp, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _vp,
+                                           _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -378,6 +402,181 @@ def tp_mlp_copy_async(dst: torch.Tensor, src: torch.Tensor, stream=None) -> torc
             raise ValueError("host tensors must be pinned (page-locked)")
     _check("tp_mlp_copy_async", _lib.tp_mlp_copy_async(_ptr(dst), _ptr(src), n, _stream(stream)))
     return dst
+
+
+# --- the paged 8-bit key/value cache (kv_cache.KvCache8 owns the buffers) -----------
+
+def _list_i32(t: Optional[torch.Tensor], what: str, n: Optional[int] = None) -> Optional[torch.Tensor]:
+    """An optional list of ints on the current CUDA device."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or not _here(t):
+        raise ValueError(f"{what} must be a contiguous 1-D int32 tensor on the current CUDA device")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{what} must have {n} entries, not {t.shape[0]}")
+    return t
+
+
+def _here(t: torch.Tensor) -> bool:
+    return t.is_cuda and t.device.index == torch.cuda.current_device()
+
+
+def _scratch(nbytes: int, stream) -> torch.Tensor:
+    """Device scratch for one call: torch hands the memory out again only to
+    work behind the call (under capture it belongs to the graph)."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if isinstance(stream, torch.cuda.Stream):
+        ws.record_stream(stream)
+    elif stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(int(stream)))
+    return ws
+
+
+def _rows(t: torch.Tensor, what: str, dims: int, tail) -> int:
+    """Row stride of a (..., heads, head_dim) tensor whose rows are dense and evenly spaced."""
+    if t.dtype not in (torch.float32, torch.bfloat16) or t.dim() != dims or tuple(t.shape[-2:]) != tuple(tail) or not _here(t):
+        raise ValueError(f"{what} must be a float32 or bfloat16 tensor (..., {tail[0]}, {tail[1]}) on the current CUDA device")
+    width = tail[0] * tail[1]
+    if t.numel() == 0:
+        return width
+    if t.stride(-1) != 1 or (tail[0] > 1 and t.stride(-2) != tail[1]):
+        raise ValueError(f"{what}: heads and head_dim must be dense")
+    lead, strides = t.shape[:-2], t.stride()[:-2]
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and strides[0] != lead[1] * strides[1]:
+        raise ValueError(f"{what}: rows must be evenly spaced")
+    if len(lead) == 1:
+        return strides[0] if lead[0] > 1 else width
+    return strides[1] if lead[1] > 1 else strides[0] if lead[0] > 1 else width
+
+
+def _kv8_dtype(t: torch.Tensor) -> int:
+    return DTYPE["f32" if t.dtype == torch.float32 else "bf16"]
+
+
+def tp_mlp_kv8_get_status(cache: Kv8Cache) -> int:
+    """The cache's status bits (KV8_FLAGS), cleared; synchronises the device."""
+    flags = _i()
+    _check("tp_mlp_kv8_get_status", _lib.tp_mlp_kv8_get_status(cache, ctypes.byref(flags)))
+    return int(flags.value)
+
+
+def tp_mlp_kv8_reserve(cache: Kv8Cache, seqs: Optional[torch.Tensor], counts: torch.Tensor, stream=None) -> None:
+    """Room for counts[i] more tokens in sequence seqs[i] (copy on write of shared last pages)."""
+    _list_i32(counts, "counts")
+    _list_i32(seqs, "seqs", counts.shape[0])
+    ws = _scratch(int(_lib.tp_mlp_kv8_pages_workspace_bytes(cache)), stream)
+    _check("tp_mlp_kv8_reserve", _lib.tp_mlp_kv8_reserve(cache, _ptr(seqs), _ptr(counts), counts.shape[0], _ptr(ws),
+                                                         ws.numel(), _stream(stream)))
+
+
+def tp_mlp_kv8_fork(cache: Kv8Cache, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
+    """children[i] (empty) becomes parents[i], sharing its pages."""
+    _list_i32(parents, "parents")
+    _list_i32(children, "children", parents.shape[0])
+    _check("tp_mlp_kv8_fork", _lib.tp_mlp_kv8_fork(cache, _ptr(parents), _ptr(children), parents.shape[0],
+                                                   _stream(stream)))
+
+
+def tp_mlp_kv8_truncate(cache: Kv8Cache, seqs: torch.Tensor, new_lengths: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Cut sequence seqs[i] to new_lengths[i] tokens (None: to none)."""
+    _list_i32(seqs, "seqs")
+    _list_i32(new_lengths, "new_lengths", seqs.shape[0])
+    _check("tp_mlp_kv8_truncate", _lib.tp_mlp_kv8_truncate(cache, _ptr(seqs), _ptr(new_lengths), seqs.shape[0],
+                                                           _stream(stream)))
+
+
+def tp_mlp_kv8_copy_pages(cache: Kv8Cache, pairs: torch.Tensor, stream=None) -> None:
+    """Copy page pairs[i, 0] to page pairs[i, 1] in every layer."""
+    if pairs.dtype != torch.int32 or pairs.dim() != 2 or pairs.shape[1] != 2 or not pairs.is_contiguous() or not _here(pairs):
+        raise ValueError("pairs must be a contiguous int32 tensor (n, 2) on the current CUDA device")
+    _check("tp_mlp_kv8_copy_pages", _lib.tp_mlp_kv8_copy_pages(cache, _ptr(pairs), pairs.shape[0], _stream(stream)))
+
+
+def tp_mlp_kv8_compact(cache: Kv8Cache, new_index: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Bring the pages in use to the pool's front; new_index[p] receives page p's new number (-1: it was free)."""
+    _list_i32(new_index, "new_index", cache.num_pages)
+    ws = _scratch(int(_lib.tp_mlp_kv8_pages_workspace_bytes(cache)), stream)
+    _check("tp_mlp_kv8_compact", _lib.tp_mlp_kv8_compact(cache, _ptr(new_index), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def tp_mlp_kv8_append(cache: Kv8Cache, layer: int, k: torch.Tensor, v: torch.Tensor,
+                      seqs: Optional[torch.Tensor] = None, cu_tokens: Optional[torch.Tensor] = None,
+                      n: Optional[int] = None, stream=None) -> None:
+    """Quantise k, v (tokens, kv_heads, head_dim) as the sequences' last tokens.  seqs gives the
+    sequences; cu_tokens (n + 1) their rows, else the rows are shared out evenly.  With neither,
+    n says how many sequences (0, 1, ...) the rows belong to (default: one token each)."""
+    tail = (cache.kv_heads, cache.head_dim)
+    stride = _rows(k, "k", 3, tail)
+    if _rows(v, "v", 3, tail) != stride or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must have one shape, dtype and row spacing")
+    _list_i32(cu_tokens, "cu_tokens")
+    if n is None:
+        n = seqs.shape[0] if seqs is not None else cu_tokens.shape[0] - 1 if cu_tokens is not None else k.shape[0]
+    _list_i32(seqs, "seqs", n)
+    _list_i32(cu_tokens, "cu_tokens", n + 1)
+    _check("tp_mlp_kv8_append", _lib.tp_mlp_kv8_append(cache, layer, _ptr(k), _ptr(v), stride, k.shape[0], _ptr(seqs),
+                                                       _ptr(cu_tokens), n, _kv8_dtype(k), _stream(stream)))
+
+
+def _kv8_query(cache: Kv8Cache, q: torch.Tensor, seqs, positions):
+    if q.dim() != 4:
+        raise ValueError("q must be (n, q_len, heads, head_dim)")
+    n, q_len, heads, _ = q.shape
+    stride = _rows(q, "q", 4, (heads, cache.head_dim))
+    _list_i32(seqs, "seqs", n)
+    _list_i32(positions, "positions", n)
+    return n, q_len, heads, stride
+
+
+def _kv8_workspace(cache: Kv8Cache, n: int, q_len: int, heads: int, stream) -> Optional[torch.Tensor]:
+    nbytes = int(_lib.tp_mlp_kv8_attention_workspace_bytes(cache, n, q_len, heads))
+    return _scratch(nbytes, stream) if nbytes else None   # 0: sizes that the call itself refuses
+
+
+def _dense(t: torch.Tensor, shape, dtype, what: str) -> torch.Tensor:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not _here(t):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {tuple(shape)} on the current CUDA device")
+    return t
+
+
+def tp_mlp_kv8_attention(cache: Kv8Cache, layer: int, q: torch.Tensor, scale: float,
+                         seqs: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of q (n, q_len, heads, head_dim) over one layer of the cache."""
+    n, q_len, heads, stride = _kv8_query(cache, q, seqs, positions)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else _dense(out, q.shape, q.dtype, "out")
+    ws = _kv8_workspace(cache, n, q_len, heads, stream)
+    _check("tp_mlp_kv8_attention",
+           _lib.tp_mlp_kv8_attention(cache, layer, _ptr(q), stride, _ptr(seqs), _ptr(positions), n, q_len, heads,
+                                     float(scale), _kv8_dtype(q), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
+                                     _stream(stream)))
+    return out
+
+
+def tp_mlp_kv8_attention_partials(cache: Kv8Cache, layer: int, q: torch.Tensor, scale: float,
+                                  seqs: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                                  maximum: Optional[torch.Tensor] = None, exp_sum: Optional[torch.Tensor] = None,
+                                  weighted: Optional[torch.Tensor] = None, stream=None):
+    """One rank's (maximum, exp_sum, weighted) of the same attention, for
+    tp_mlp_merge_attention_partials; shaped like q without and with its last axis."""
+    n, q_len, heads, stride = _kv8_query(cache, q, seqs, positions)
+
+    def stat(t, what):
+        if t is None:
+            return torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        return _dense(t, q.shape[:3], torch.float32, what)
+
+    maximum, exp_sum = stat(maximum, "maximum"), stat(exp_sum, "exp_sum")
+    weighted = torch.empty(q.shape, dtype=q.dtype, device=q.device) if weighted is None else \
+        _dense(weighted, q.shape, q.dtype, "weighted")
+    ws = _kv8_workspace(cache, n, q_len, heads, stream)
+    _check("tp_mlp_kv8_attention_partials",
+           _lib.tp_mlp_kv8_attention_partials(cache, layer, _ptr(q), stride, _ptr(seqs), _ptr(positions), n, q_len,
+                                              heads, float(scale), _kv8_dtype(q), _ptr(maximum), _ptr(exp_sum),
+                                              _ptr(weighted), _ptr(ws), 0 if ws is None else ws.numel(),
+                                              _stream(stream)))
+    return maximum, exp_sum, weighted
 
 
 # --- convenience wrapper -----------------------------------------------------------
