@@ -1,123 +1,813 @@
 // kv8_attention.cu -- attention over the paged 8-bit key/value cache.
 //
-// For query row r (query j of an entry, head h) and the tokens t that it sees:
-//   s_t = scale * k_scale * (q . k_t),  m = max s_t,  p_t = exp(s_t - m),
+// For a query row (query j of an entry, head h) and the tokens t that it sees:
+//   s_t = scale * k_scale * (q . k_t),   m = max s_t,   p_t = exp(s_t - m),
 //   out = sum p_t v_scale v_t / sum p_t.
-// One CTA per query row walks the sequence 128 tokens at a time with a running
-// maximum and sum: a thread scores one token, then owns output columns.
+//
+// A decode step reads every cached byte once and does 4 * rows flops with it,
+// rows = q_len * heads / kv_heads: HBM-bound.  The kernel's shape follows from
+// keeping the loads going:
+//
+// * The work is a row of steps of 16 tokens -- entry by entry, KV head by KV
+//   head, tile of query rows by tile -- cut evenly over all warps of the GPU
+//   (prefix sums over the lengths, on the device: the lengths are not known to
+//   the host).  A warp owns its steps: it streams their keys and values through
+//   a ring of its own in shared memory (cp.async, no block-wide barrier) and
+//   keeps running maxima, sums and outputs in registers.
+// * Both products are mma.m16n8k16 with the tokens (or the value columns) as
+//   the M side and 8 query rows as N, so a group of up to 8 heads fills the
+//   tile.  e4m3 to fp16 is exact.  Keys: a thread's 16 loaded bytes are the
+//   k-elements of four mma steps (the head dimension may be taken in any order,
+//   the same one for the queries).  Values: two tokens' bytes are interleaved
+//   (prmt) into the (token, token + 1) pairs that the A operand holds, and a
+//   thread ends up with head_dim / 8 consecutive output columns.  The weights
+//   turn from the first product's C layout to the second's B layout by
+//   movmatrix; nothing passes through shared memory between the products.
+// * The scales are constant over a step (a step lies in one page): the key
+//   scale multiplies the scores, the value scale the weights.
+//
+// Precision.  Queries are brought to [1, 2) by a power of two per row and
+// held in fp16, exactly for bf16 input (but for elements 2^-14 below the row's
+// largest, whose error is 2^-25 of it); fp32 input is held as two fp16 parts
+// (22 bits).  The running reference R is the maximum of s_t + log2(v_scale's
+// binade), in base-2 logs, so that the weight that multiplies the values,
+// w_t = 2^(s_t - R) v_scale, is at most 2^8 whatever the pages' scales; it is
+// rounded to fp16 for bf16 results (2^-11, under the result's 2^-8) and held as
+// two parts for fp32.  R moves only when a score exceeds it by 2^8 (one vote a
+// step; the sums are rescaled then).  Scores, sums and outputs are fp32.
+//
+// Warps whose pieces meet in one segment (entry, KV head, row tile) join them
+// in shared memory; pieces of a segment that CTAs share go to the workspace (at
+// most two per CTA) and a second kernel joins them, in order, so the result
+// does not depend on timing.  Masked places: bytes behind a sequence's end are
+// never loaded (zero-filled), a masked score is -inf before it is used, and a
+// NaN value that only some rows see is taken out of the product and put into
+// just their outputs.
 #include <math.h>
 
 #include "common.cuh"
 #include "internal.h"
 #include "kv8.cuh"
+#include "tc_ptx.cuh"
+#include "vec_io.cuh"
 
 namespace tpmlp {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMaxDim = 256;
+constexpr int kStep = 16;            // tokens of one step
+constexpr float kSlack = 8.f;        // how far (base-2 logs) a score may exceed the reference
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
+constexpr int kCombineThreads = 256;
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attention_rows_kernel(Kv8 c, Kv8Query a) {
-    __shared__ float qs[kMaxDim], ps[kThreads], red[kThreads];
-    __shared__ int pages[kThreads / 16];
+// Shared memory: [ring of every warp | first piece of every warp | prefix of the entries' steps | piece table].  A warp
+// leaves at most two pieces, at the start and at the end of its steps; the second lies in its ring, which is idle then.
+template <int D, int NT>
+struct Cfg {
+    static constexpr int kWarps = 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kStage = 2 * kStep * D;                       // keys and values of one step
+    static constexpr int kStages = D == 256 ? 2 : D == 128 ? 4 : 6;
+    static constexpr int kRing = kStage * kStages;
+    static constexpr int kPad = D + 4;                                  // floats a piece's row takes
+    static constexpr int kPiece = kRows * (kPad + 4) * 4;               // outputs, reference, sum, maximum
+    static_assert(kPiece <= kRing, "the second piece lies in the ring");
+    static constexpr size_t smem(int n) { return (size_t)kWarps * (kRing + kPiece) + (n + 2) / 2 * 2 * 8 + kWarps * 2 * 4; }
+};
+
+// Workspace: [header: total steps, CTAs at work | prefix, n + 1 | two pieces per CTA]
+struct Split {
+    long long *total;      // [0] steps, [1] CTAs
+    long long *prefix;
+    float *pieces;
+};
+
+struct Entry {             // one entry of the call's list
+    int seq, len, seen;    // seen: tokens that its last query sees; seq -1: passed over
+    long long first;       // position of its query 0
+};
+
+__device__ __forceinline__ Entry load_entry(const Kv8 &c, const Kv8Query &a, int i, int *bad) {
+    Entry e;
+    e.seq = kv8_seq(a.seqs, i);
+    e.len = e.seen = 0;
+    e.first = 0;
+    if (e.seq == -1) return e;
+    if ((unsigned)e.seq >= (unsigned)c.max_seqs) {
+        *bad |= TP_MLP_KV8_BAD_SEQUENCE;
+        e.seq = -1;
+        return e;
+    }
+    e.len = c.lengths[e.seq];
+    if (e.len < 0 || e.len > c.capacity()) {
+        *bad |= TP_MLP_KV8_BAD_LENGTH;
+        e.seq = -1;
+        e.len = 0;
+        return e;
+    }
+    e.first = a.positions ? (long long)a.positions[i] : (long long)e.len - a.q_len;
+    e.seen = (int)max(0LL, min((long long)e.len, e.first + a.q_len));
+    return e;
+}
+
+// --- register-level pieces ------------------------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
+    const int bytes = take ? 16 : 0;   // 0: the 16 bytes are filled with zeros
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
+    return v;
+}
+// four e4m3 bytes -> two f16x2 (bytes 0,1 and 2,3), exact
+__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 widen_f16x2(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Bytes of w that are e4m3 NaN, as 0xff each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+// Byte offset of 16-byte chunk ch of row `row` in a stage's keys or values.  For
+// rows of 128 bytes and more the chunks are swizzled so that the 8 lanes of a
+// load phase (two neighbouring rows of keys with chunks 2t + const, or four
+// even rows of values with two chunks) touch 8 different 16-byte banks.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
+    return (uint32_t)(row * D + ((D >= 128 ? ch ^ (row & 7) : ch) << 4));
+}
+// The chunk of a key row that thread t of a quad takes as its i-th.
+template <int D>
+__device__ __forceinline__ int key_chunk(int t, int i) {
+    return D == 64 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
+}
+
+// Eight query elements as fp32.
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *f) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
+    f[4] = bf16lo(u.z); f[5] = bf16hi(u.z); f[6] = bf16lo(u.w); f[7] = bf16hi(u.w);
+}
+__device__ __forceinline__ void load8(const float *p, float *f) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// Where row r (0 .. q_len * group - 1) of (entry, KV head) is in q and the outputs.
+struct RowMap {
+    int entry, kv_head, group, q_len, heads;
+    __device__ __forceinline__ int query(int r) const { return r / group; }
+    __device__ __forceinline__ long long out_row(int r) const {
+        const int j = r / group;
+        return ((long long)entry * q_len + j) * heads + kv_head * group + (r - j * group);
+    }
+};
+
+// A row's statistics in the result's terms.  ref: reference R, sum: sum of
+// 2^(s - R), top: the row's true maximum score (base-2 logs).
+struct RowResult {
+    float factor;          // what the accumulated outputs are multiplied with
+    float maximum, exp_sum;
+};
+__device__ __forceinline__ RowResult row_result(float ref, float sum, float top, bool partial) {
+    RowResult r;
+    if (!partial) {
+        r.factor = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // nothing seen: zeros; NaN stays
+        return r;
+    }
+    if (top == -INFINITY && sum == 0.f) {
+        r.factor = 0.f;
+        r.maximum = -INFINITY;
+        r.exp_sum = 0.f;
+        return r;
+    }
+    r.factor = exp2f(ref - top);
+    r.exp_sum = sum * r.factor;
+    r.maximum = isnan(sum) && top != INFINITY ? sum : top * kLn2;
+    return r;
+}
+
+// --- the streaming kernel ----------------------------------------------------------
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    attention_kernel(Kv8 c, Kv8Query a, Split ws, int row_tiles) {
+    using C = Cfg<D, NT>;
+    constexpr bool kExact = sizeof(T) == 4;       // two fp16 parts for queries and weights
+    constexpr int kParts = kExact ? 2 : 1;
+    constexpr int kKs = D / 16;                   // mma steps of the score product
+    constexpr int kMt = D / 16;                   // 16-column tiles of the output product
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int n = a.n, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int group = a.heads / c.kv_heads, rows = a.q_len * group;
+    const int units_per_entry = c.kv_heads * row_tiles;
+    const uint32_t ring = tc::smem_u32(smem) + warp * C::kRing;
+    auto piece_at = [&](int w, int p) {
+        return reinterpret_cast<float *>(smem + (p ? (size_t)w * C::kRing : (size_t)C::kWarps * C::kRing + (size_t)w * C::kPiece));
+    };
+    long long *prefix = reinterpret_cast<long long *>(smem + (size_t)C::kWarps * (C::kRing + C::kPiece));
+    int *piece_seg = reinterpret_cast<int *>(prefix + (n + 2) / 2 * 2);
+    __shared__ long long scan_part[C::kWarps];
+
     pdl_allow_dependents();
     pdl_wait_previous();
-    const int tid = threadIdx.x, D = c.head_dim;
-    const int h = blockIdx.x % a.heads, j = blockIdx.x / a.heads % a.q_len, i = blockIdx.x / a.heads / a.q_len;
-    const int seq = kv8_seq(a.seqs, i);
-    if (seq == -1) return;
-    if ((unsigned)seq >= (unsigned)c.max_seqs) {
-        if (tid == 0) kv8_flag(c, TP_MLP_KV8_BAD_SEQUENCE);
-        return;
-    }
-    const int len = c.lengths[seq];
-    if (len < 0 || len > c.capacity()) {
-        if (tid == 0) kv8_flag(c, TP_MLP_KV8_BAD_LENGTH);
-        return;
-    }
-    const long long pos = (a.positions ? (long long)a.positions[i] : (long long)len - a.q_len) + j;
-    const int end = (int)max(0LL, min((long long)len, pos + 1));
-    const int kvh = h / (a.heads / c.kv_heads);
-    const T *q = static_cast<const T *>(a.q) + ((long long)i * a.q_len + j) * a.row_stride + (long long)h * D;
-    for (int d = tid; d < D; d += kThreads) qs[d] = to_f32(q[d]) * a.scale;
-    float m = -INFINITY, l = 0.f, o[kMaxDim / kThreads] = {0.f, 0.f};
-    for (int t0 = 0; t0 < end; t0 += kThreads) {
+
+    // 1. steps of every entry, and their prefix sums
+    {
+        constexpr int kPer = kMaxList / C::kThreads;
+        long long mine[kPer], sum = 0;
+        int bad = 0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int i = tid * kPer + u;
+            mine[u] = sum;
+            if (i < n) sum += (long long)((load_entry(c, a, i, &bad).seen + kStep - 1) / kStep) * units_per_entry;
+        }
+        if (bad && blockIdx.x == 0) kv8_flag(c, bad);
+        long long x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) scan_part[warp] = x;
         __syncthreads();
-        if (tid < kThreads / 16) {
-            const int t = t0 + tid * 16;
-            int p = -1;
-            if (t < end) {
-                p = c.table[(long long)seq * c.max_pages + (t >> c.page_shift)];
-                if ((unsigned)p >= (unsigned)c.num_pages) {
-                    kv8_flag(c, TP_MLP_KV8_BAD_PAGE);
-                    p = -1;
+        long long base = x - sum;
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) base += w < warp ? scan_part[w] : 0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u)
+            if (tid * kPer + u <= n) prefix[tid * kPer + u] = base + mine[u];
+        if (n == kMaxList && tid == C::kThreads - 1) prefix[n] = base + sum;
+        if (lane < 2) piece_seg[warp * 2 + lane] = -1;
+        __syncthreads();
+    }
+    const long long total = prefix[n];
+    const long long ctas = max(1LL, min((long long)gridDim.x, (total + C::kWarps - 1) / C::kWarps));
+    if (blockIdx.x == 0) {
+        for (int i = tid; i <= n; i += C::kThreads) ws.prefix[i] = prefix[i];
+        if (tid == 0) {
+            ws.total[0] = total;
+            ws.total[1] = ctas;
+        }
+    }
+    if (blockIdx.x >= ctas || total == 0) return;
+    const long long c0 = total * blockIdx.x / ctas, c1 = total * (blockIdx.x + 1) / ctas;
+    const long long w0 = c0 + (c1 - c0) * warp / C::kWarps, w1 = c0 + (c1 - c0) * (warp + 1) / C::kWarps;
+
+    // 2. this warp's steps, segment by segment
+    int e = 0;
+    if (w0 < w1) {   // the entry that holds step w0: the last with prefix <= w0
+        int lo = 0, hi = n;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= w0) lo = mid;
+            else hi = mid;
+        }
+        e = lo;
+    }
+    int n_pieces = 0;
+    for (long long at = w0; at < w1;) {
+        while (prefix[e + 1] <= at) ++e;
+        const long long entry0 = prefix[e];
+        const int steps = (int)((prefix[e + 1] - entry0) / units_per_entry);
+        const int unit = (int)((at - entry0) / steps);
+        const long long seg0 = entry0 + (long long)unit * steps;
+        const int s0 = (int)(at - seg0), s1 = (int)min((long long)steps, w1 - seg0);
+        at = seg0 + s1;
+        const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
+        int bad = 0;
+        const Entry en = load_entry(c, a, e, &bad);
+        const RowMap map = {e, kv_head, group, a.q_len, a.heads};
+
+        // queries: row g of each n-tile, this thread's columns of every k-step
+        uint32_t q[kParts][NT][kKs][2];
+        float fac[NT][2];
+        int limit[NT][2];      // tokens that the column's row sees
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = (tile * NT + nt) * 8 + g;
+            const bool have = r < rows;
+            const int rr = have ? r : 0, j = map.query(rr);
+            const T *src = static_cast<const T *>(a.q) + ((long long)e * a.q_len + j) * a.row_stride +
+                           (long long)(kv_head * group + rr - j * group) * D;
+            float f[D / 4];
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                load8(src + key_chunk<D>(t, i) * 16, f + 16 * i);
+                load8(src + key_chunk<D>(t, i) * 16 + 8, f + 16 * i + 8);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(f[i]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+            ex = ex > 127 ? 0 : max(ex, -126);   // an infinite row stays as it is
+            const float scale_down = ex == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - ex) << 23);   // 2^-ex
+#pragma unroll
+            for (int k = 0; k < kKs; ++k) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float v0 = have ? f[4 * k + 2 * x] * scale_down : 0.f;
+                    const float v1 = have ? f[4 * k + 2 * x + 1] * scale_down : 0.f;
+                    q[0][nt][k][x] = f16x2(v0, v1);
+                    if (kExact) {
+                        const float2 h = widen_f16x2(q[0][nt][k][x]);
+                        q[kParts - 1][nt][k][x] = f16x2(v0 - h.x, v1 - h.y);
+                    }
                 }
             }
-            pages[tid] = p;
-        }
-        __syncthreads();
-        const int t = t0 + tid, p = pages[tid >> 4];
-        float s = -INFINITY;
-        if (t < end && p >= 0) {
-            const long long head = (long long)p * c.kv_heads + kvh;
-            const uint32_t *k = reinterpret_cast<const uint32_t *>(c.k + (head * c.page_size + (t & (c.page_size - 1))) * D);
-            float acc = 0.f;
-            for (int d = 0; d < D / 4; ++d) {
-                const float4 f = e4m3_unpack4(k[d]);
-                acc += f.x * qs[4 * d] + f.y * qs[4 * d + 1] + f.z * qs[4 * d + 2] + f.w * qs[4 * d + 3];
+            const float up = have ? ldexpf(a.scale * kLog2e, ex) : 0.f;
+            const int lim = have ? (int)max(0LL, min((long long)en.len, en.first + j + 1)) : 0x7fffffff;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                fac[nt][x] = __shfl_sync(0xffffffffu, up, (2 * t + x) * 4);
+                limit[nt][x] = __shfl_sync(0xffffffffu, lim, (2 * t + x) * 4);
             }
-            s = acc * c.k_scale[head];
         }
-        red[tid] = s;
-        __syncthreads();
-        for (int w = kThreads / 2; w > 0; w >>= 1) {
-            if (tid < w) red[tid] = fmaxf(red[tid], red[tid + w]);
-            __syncthreads();
+        // steps below `plain` need no mask: the tile's first row sees the fewest tokens
+        const int least = (int)max(0LL, min((long long)en.len, en.first + map.query(tile * C::kRows) + 1));
+        const int plain = least / kStep;
+
+        float o[NT][kMt][4], ref[NT][2], sum[NT][2], top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int m = 0; m < kMt; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[nt][m][k] = 0.f;
+            ref[nt][0] = ref[nt][1] = top[nt][0] = top[nt][1] = -INFINITY;
+            sum[nt][0] = sum[nt][1] = 0.f;
         }
-        const float top = fmaxf(m, red[0]);
-        const float base = top == -INFINITY ? 0.f : top;
-        const float turn = expf(m - base);
-        m = top;
-        ps[tid] = expf(s - base);
-        __syncthreads();
-        l *= turn;
-        for (int x = 0; x < kThreads; ++x) l += ps[x];
-        for (int u = 0; u < kMaxDim / kThreads; ++u) {
-            const int d = tid + u * kThreads;
-            if (d >= D) break;
-            float acc = o[u] * turn;
-            for (int x = 0; x < kThreads && t0 + x < end; ++x) {
-                const int pg = pages[x >> 4];
-                if (pg < 0) continue;
-                const long long head = (long long)pg * c.kv_heads + kvh;
-                const uint8_t code = c.v[(head * c.page_size + ((t0 + x) & (c.page_size - 1))) * D + d];
-                const float v = __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
-                acc += ps[x] * c.v_scale[head] * v;
+
+        // pages come 32 at a time: lane x holds the x-th one's number and scales.  The loads run ahead of the
+        // products by fewer than 32 steps, so the products are in this batch or in the one before.
+        const int *row = c.table + (long long)en.seq * c.max_pages;
+        const int page_steps = c.page_shift - 4;            // log2(steps of a page)
+        const int n_pages = c.pages_of(en.len);
+        int batch = -1, page = 0;
+        float ks = 0.f, vs = 0.f, ks_before = 0.f, vs_before = 0.f;
+        auto fetch = [&](int s, int slot) {
+            const int nth = s >> page_steps;
+            if ((nth >> 5) != batch) {
+                batch = nth >> 5;
+                ks_before = ks;
+                vs_before = vs;
+                const int mine = batch * 32 + lane;
+                page = mine < n_pages ? row[mine] : 0;
+                const bool ok = (unsigned)page < (unsigned)c.num_pages;
+                if (!ok && mine <= (s1 - 1) >> page_steps) kv8_flag(c, TP_MLP_KV8_BAD_PAGE);
+                page = ok ? page : -1;
+                const long long head = (long long)(ok ? page : 0) * c.kv_heads + kv_head;
+                ks = c.k_scale[head];
+                vs = ok ? c.v_scale[head] : -1.f;           // negative: not a page of the pool
             }
-            o[u] = acc;
+            const int p = __shfl_sync(0xffffffffu, page, nth & 31);
+            const long long off = (((long long)(p < 0 ? 0 : p) * c.kv_heads + kv_head) * c.page_size +
+                                   ((s * kStep) & (c.page_size - 1))) * D;
+            const int live = p < 0 ? 0 : en.len - s * kStep;   // rows behind the end are zeros
+            const uint32_t dst = ring + slot * C::kStage;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int x = i * 32 + lane, r = x / (D / 16), ch = x % (D / 16);
+                cp_async16(dst + chunk_at<D>(r, ch), c.k + off + 16 * x, r < live);
+                cp_async16(dst + kStep * D + chunk_at<D>(r, ch), c.v + off + 16 * x, r < live);
+            }
+        };
+        int slot = 0;
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) {
+            if (s0 + i < s1) fetch(s0 + i, i);
+            cp_commit();
+        }
+        for (int s = s0; s < s1; ++s) {
+            cp_wait<C::kStages - 2>();
+            __syncwarp();
+            // (every lane is done with the slot that this fetch refills: it was read a step ago)
+            if (s + C::kStages - 1 < s1) fetch(s + C::kStages - 1, slot == 0 ? C::kStages - 1 : slot - 1);
+            cp_commit();
+            const uint32_t keys = ring + slot * C::kStage, vals = keys + kStep * D;
+            slot = slot + 1 == C::kStages ? 0 : slot + 1;
+            const int nth = s >> page_steps;
+            const bool current = (nth >> 5) == batch;
+            const float kscale = __shfl_sync(0xffffffffu, current ? ks : ks_before, nth & 31);
+            const float vscale = __shfl_sync(0xffffffffu, current ? vs : vs_before, nth & 31);
+            if (vscale < 0.f) continue;                     // none of this page's tokens is seen
+
+            // scores: 16 tokens x 8 rows a tile
+            float sc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 lo4 = lds128(keys + chunk_at<D>(g, key_chunk<D>(t, i)));
+                const uint4 hi4 = lds128(keys + chunk_at<D>(g + 8, key_chunk<D>(t, i)));
+                const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3_to_f16(lo[w], a0, a2);
+                    e4m3_to_f16(hi[w], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int pt = 0; pt < kParts; ++pt)
+                            mma(sc[nt], a0, a1, a2, a3, q[pt][nt][4 * i + w][0], q[pt][nt][4 * i + w][1]);
+                }
+            }
+            // base-2 scores; the binade above the value scale
+            const int vexp = max((int)(__float_as_uint(vscale) >> 23) - 126, -100);
+            const float vlog = (float)vexp;
+            const bool masked = s >= plain;
+            bool rise = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float x = sc[nt][k] * (fac[nt][k & 1] * kscale);
+                    if (masked && s * kStep + g + 8 * (k >> 1) >= limit[nt][k & 1]) x = -INFINITY;
+                    sc[nt][k] = x;
+                    rise |= x + vlog > ref[nt][k & 1] + kSlack;
+                    top[nt][k & 1] = fmaxf(top[nt][k & 1], x);
+                }
+            if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float m = fmaxf(sc[nt][x], sc[nt][x + 2]);
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        m = fmaxf(ref[nt][x], m + vlog);
+                        const float turn = m == ref[nt][x] ? 1.f : exp2_fast(ref[nt][x] - m);
+                        ref[nt][x] = m;
+                        sum[nt][x] *= turn;
+#pragma unroll
+                        for (int mt = 0; mt < kMt; ++mt) {
+                            o[nt][mt][x] *= turn;
+                            o[nt][mt][x + 2] *= turn;
+                        }
+                    }
+            }
+            uint32_t w[kParts][NT][2];      // weights as the second product's B operand
+            uint32_t see[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float r = ref[nt][k & 1];
+                    p[k] = exp2_fast(sc[nt][k] - (r == -INFINITY ? 0.f : r));
+                    sum[nt][k & 1] += p[k];
+                    p[k] *= vscale;
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t h = f16x2(p[2 * x], p[2 * x + 1]);
+                    w[0][nt][x] = transpose8x8(h);
+                    if (kExact) {
+                        const float2 b = widen_f16x2(h);
+                        w[kParts - 1][nt][x] = transpose8x8(f16x2(p[2 * x] - b.x, p[2 * x + 1] - b.y));
+                    }
+                }
+            }
+
+            // outputs: tokens 2t, 2t+1, 2t+8, 2t+9 of this thread, D / 8 columns from g on
+            uint32_t v[4][D / 32];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 2 * t + (k & 1) + 8 * (k >> 1);
+                if (D == 64) {
+                    const uint2 x = lds64(vals + r * D + g * 8);
+                    v[k][0] = x.x;
+                    v[k][1] = x.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i) {
+                        const uint4 x = lds128(vals + chunk_at<D>(r, g + 8 * i));
+                        v[k][4 * i] = x.x;
+                        v[k][4 * i + 1] = x.y;
+                        v[k][4 * i + 2] = x.z;
+                        v[k][4 * i + 3] = x.w;
+                    }
+                }
+            }
+            if (masked) {   // a NaN value must not reach rows that do not see its token (0 * NaN)
+                uint32_t any = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) any |= nan_bytes(v[k][i]);
+                if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int tok = s * kStep + g + 8 * x;
+                            see[nt][x] = transpose8x8(f16x2(tok < limit[nt][0] ? 1.f : 0.f, tok < limit[nt][1] ? 1.f : 0.f));
+                        }
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t nb[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            nb[k] = nan_bytes(v[k][i]);
+                            v[k][i] &= ~nb[k];
+                            nb[k] &= 0x38383838u;           // e4m3's 1
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t sel = h ? 0x7362u : 0x5140u;
+                            uint32_t a0, a1, a2, a3;
+                            e4m3_to_f16(__byte_perm(nb[0], nb[1], sel), a0, a1);
+                            e4m3_to_f16(__byte_perm(nb[2], nb[3], sel), a2, a3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma(hit, a0, a1, a2, a3, see[nt][0], see[nt][1]);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (hit[k] > 0.f) o[nt][2 * i + h][k] = NAN;
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t sel = h ? 0x7362u : 0x5140u;   // (token, token + 1) pairs of two columns
+                    uint32_t a0, a1, a2, a3;
+                    e4m3_to_f16(__byte_perm(v[0][i], v[1][i], sel), a0, a1);
+                    e4m3_to_f16(__byte_perm(v[2][i], v[3][i], sel), a2, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int pt = 0; pt < kParts; ++pt)
+                            mma(o[nt][2 * i + h], a0, a1, a2, a3, w[pt][nt][0], w[pt][nt][1]);
+                }
+        }
+        cp_wait<0>();
+        __syncwarp();   // the ring is free for the next segment
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int m = 4; m < 32; m <<= 1) {
+                    sum[nt][x] += __shfl_xor_sync(0xffffffffu, sum[nt][x], m);
+                    top[nt][x] = fmaxf(top[nt][x], __shfl_xor_sync(0xffffffffu, top[nt][x], m));
+                }
+
+        // 3. a whole segment is written; a piece of one goes to shared memory.  The thread's column of output
+        // product 2 i + h, element pair (x, x + 2), is column(i) + 2 h (+ 1).
+        const bool whole = s0 == 0 && s1 == steps;
+        float *piece = piece_at(warp, n_pieces);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int in_tile = nt * 8 + 2 * t + x, r = tile * C::kRows + in_tile;
+                float factor = 1.f;
+                T *dst = nullptr;
+                if (whole) {
+                    if (r >= rows) continue;
+                    const long long orow = map.out_row(r);
+                    const RowResult res = row_result(ref[nt][x], sum[nt][x], top[nt][x], a.maximum != nullptr);
+                    factor = res.factor;
+                    dst = static_cast<T *>(a.o) + orow * D;
+                    if (a.maximum && g == 0) {
+                        a.maximum[orow] = res.maximum;
+                        a.exp_sum[orow] = res.exp_sum;
+                    }
+                } else if (g == 0) {
+                    float *stat = piece + C::kRows * C::kPad + in_tile * 4;
+                    stat[0] = ref[nt][x];
+                    stat[1] = sum[nt][x];
+                    stat[2] = top[nt][x];
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int col = D == 64 ? g * 8 + 4 * i : 128 * (i >> 2) + g * 16 + 4 * (i & 3);
+                    const float4 v4 = make_float4(o[nt][2 * i][x] * factor, o[nt][2 * i][x + 2] * factor,
+                                                  o[nt][2 * i + 1][x] * factor, o[nt][2 * i + 1][x + 2] * factor);
+                    if (whole) store4(dst + col, v4);
+                    else *reinterpret_cast<float4 *>(piece + in_tile * C::kPad + col) = v4;
+                }
+            }
+        if (!whole) {
+            if (lane == 0) piece_seg[warp * 2 + n_pieces] = e * units_per_entry + unit;
+            ++n_pieces;
         }
     }
-    const long long row = ((long long)i * a.q_len + j) * a.heads + h;
-    const float inv = a.maximum ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
-    for (int u = 0; u < kMaxDim / kThreads; ++u) {
-        const int d = tid + u * kThreads;
-        if (d < D) static_cast<T *>(a.o)[row * D + d] = from_f32<T>(o[u] * inv);
+    __syncthreads();
+
+    // 4. join the pieces of each segment, in order; pieces that other CTAs share go to the workspace
+    for (int first = 0; first < 2 * C::kWarps;) {
+        const int seg = piece_seg[first];
+        int last = first + 1;   // a segment's pieces are neighbours but for unused places
+        if (seg < 0) {
+            first = last;
+            continue;
+        }
+        while (last < 2 * C::kWarps && (piece_seg[last] == seg || piece_seg[last] < 0)) ++last;
+        const int se = seg / units_per_entry, unit = seg - se * units_per_entry;
+        const long long entry0 = prefix[se];
+        const int steps = (int)((prefix[se + 1] - entry0) / units_per_entry);
+        const long long seg0 = entry0 + (long long)unit * steps;
+        const bool whole = seg0 >= c0 && seg0 + steps <= c1;
+        const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
+        const RowMap map = {se, kv_head, group, a.q_len, a.heads};
+        float *out = ws.pieces + ((size_t)blockIdx.x * 2 + (seg0 < c0 ? 0 : 1)) * (C::kRows * (D + 4));
+        for (int x = tid; x < C::kRows * (D / 4); x += C::kThreads) {
+            const int in_tile = x / (D / 4), col = (x - in_tile * (D / 4)) * 4;
+            float r = -INFINITY, tp = -INFINITY;
+            for (int p = first; p < last; ++p) {
+                if (piece_seg[p] < 0) continue;
+                const float *stat = piece_at(p >> 1, p & 1) + C::kRows * C::kPad + in_tile * 4;
+                r = fmaxf(r, stat[0]);
+                tp = fmaxf(tp, stat[2]);
+            }
+            float l = 0.f;
+            float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = first; p < last; ++p) {
+                if (piece_seg[p] < 0) continue;
+                const float *pc = piece_at(p >> 1, p & 1);
+                const float *stat = pc + C::kRows * C::kPad + in_tile * 4;
+                const float f = stat[0] == r ? 1.f : exp2f(stat[0] - r);   // (-inf twice is 1, on sums of 0)
+                l += stat[1] * f;
+                const float4 y = *reinterpret_cast<const float4 *>(pc + in_tile * C::kPad + col);
+                v4.x += y.x * f;
+                v4.y += y.y * f;
+                v4.z += y.z * f;
+                v4.w += y.w * f;
+            }
+            if (whole) {
+                const int rr = tile * C::kRows + in_tile;
+                if (rr < rows) {
+                    const long long orow = map.out_row(rr);
+                    const RowResult res = row_result(r, l, tp, a.maximum != nullptr);
+                    store4(static_cast<T *>(a.o) + orow * D + col,
+                           make_float4(v4.x * res.factor, v4.y * res.factor, v4.z * res.factor, v4.w * res.factor));
+                    if (a.maximum && col == 0) {
+                        a.maximum[orow] = res.maximum;
+                        a.exp_sum[orow] = res.exp_sum;
+                    }
+                }
+            } else {
+                *reinterpret_cast<float4 *>(out + in_tile * D + col) = v4;
+                if (col == 0) *reinterpret_cast<float4 *>(out + C::kRows * D + in_tile * 4) = make_float4(r, l, tp, 0.f);
+            }
+        }
+        first = last;
     }
-    if (a.maximum && tid == 0) {
-        a.maximum[row] = isnan(l) && m != INFINITY ? l : m;   // (fmaxf passes over a NaN score)
-        a.exp_sum[row] = l;
+}
+
+// Joins the pieces of the segments that several CTAs share, and writes the rows of entries that see nothing.  One CTA
+// per segment.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_kernel(Kv8 c, Kv8Query a, Split ws, int row_tiles) {
+    using C = Cfg<D, NT>;
+    pdl_allow_dependents();
+    pdl_wait_previous();
+    const int units_per_entry = c.kv_heads * row_tiles;
+    const int e = blockIdx.x / units_per_entry, unit = blockIdx.x - e * units_per_entry;
+    const int group = a.heads / c.kv_heads, rows = a.q_len * group;
+    const long long entry0 = ws.prefix[e], total = ws.total[0], ctas = ws.total[1];
+    const int steps = (int)((ws.prefix[e + 1] - entry0) / units_per_entry);
+    long long from = 0, to = -1;
+    if (steps > 0) {
+        const long long seg0 = entry0 + (long long)unit * steps;
+        from = ((seg0 + 1) * ctas - 1) / total;               // the CTA that holds a step x: total*cta/ctas <= x
+        to = ((seg0 + steps) * ctas - 1) / total;
+        if (from == to) return;                                // joined there
+    } else {
+        int bad = 0;
+        if (load_entry(c, a, e, &bad).seq < 0) return;         // its rows stay as they were
     }
+    const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
+    const RowMap map = {e, kv_head, group, a.q_len, a.heads};
+    for (int x = threadIdx.x; x < C::kRows * (D / 4); x += kCombineThreads) {
+        const int in_tile = x / (D / 4), col = (x - in_tile * (D / 4)) * 4, rr = tile * C::kRows + in_tile;
+        if (rr >= rows) continue;
+        float r = -INFINITY, tp = -INFINITY, l = 0.f;
+        for (long long p = from; p <= to; ++p) {
+            const float *stat = ws.pieces + ((size_t)p * 2 + (p == from ? 1 : 0)) * (C::kRows * (D + 4)) + C::kRows * D;
+            r = fmaxf(r, stat[in_tile * 4]);
+            tp = fmaxf(tp, stat[in_tile * 4 + 2]);
+        }
+        float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (long long p = from; p <= to; ++p) {
+            const float *pc = ws.pieces + ((size_t)p * 2 + (p == from ? 1 : 0)) * (C::kRows * (D + 4));
+            const float4 stat = *reinterpret_cast<const float4 *>(pc + C::kRows * D + in_tile * 4);
+            const float4 y = *reinterpret_cast<const float4 *>(pc + in_tile * D + col);
+            const float f = stat.x == r ? 1.f : exp2f(stat.x - r);
+            l += stat.y * f;
+            v4.x += y.x * f;
+            v4.y += y.y * f;
+            v4.z += y.z * f;
+            v4.w += y.w * f;
+        }
+        const long long orow = map.out_row(rr);
+        const RowResult res = row_result(r, l, tp, a.maximum != nullptr);
+        store4(static_cast<T *>(a.o) + orow * D + col,
+               make_float4(v4.x * res.factor, v4.y * res.factor, v4.z * res.factor, v4.w * res.factor));
+        if (a.maximum && col == 0) {
+            a.maximum[orow] = res.maximum;
+            a.exp_sum[orow] = res.exp_sum;
+        }
+    }
+}
+
+Split split_of(void *ws, int n) {
+    char *p = static_cast<char *>(ws);
+    Split s;
+    s.total = reinterpret_cast<long long *>(p);
+    s.prefix = reinterpret_cast<long long *>(p + 256);
+    s.pieces = reinterpret_cast<float *>(p + 256 + align256((size_t)(n + 1) * 8));
+    return s;
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_tile(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
+    using C = Cfg<D, NT>;
+    const int rows = a.q_len * (a.heads / c.kv_heads), row_tiles = (rows + C::kRows - 1) / C::kRows;
+    const Split s = split_of(ws, a.n);
+    auto kern = attention_kernel<T, D, NT>;
+    cudaError_t e = ensure_smem_attr(kern, C::smem(kMaxList));
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3((unsigned)num_sms), dim3(C::kThreads), C::smem(a.n), st, c, a, s, row_tiles);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(combine_kernel<T, D, NT>, dim3((unsigned)((long long)a.n * c.kv_heads * row_tiles)),
+                      dim3(kCombineThreads), 0, st, c, a, s, row_tiles);
+}
+
+// Row tiles of 8 while a group's rows fit one, else as wide as the registers hold.
+template <int D> constexpr int wide_tiles() { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+
+template <typename T, int D>
+cudaError_t launch_dim(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
+    const int rows = a.q_len * (a.heads / c.kv_heads);
+    if (rows <= 8 || wide_tiles<D>() == 1) return launch_tile<T, D, 1>(c, a, ws, num_sms, st);
+    if (rows <= 16 || wide_tiles<D>() == 2) return launch_tile<T, D, (wide_tiles<D>() > 1 ? 2 : 1)>(c, a, ws, num_sms, st);
+    return launch_tile<T, D, wide_tiles<D>()>(c, a, ws, num_sms, st);
+}
+
+template <typename T>
+cudaError_t launch_typed(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
+    if (c.head_dim == 64) return launch_dim<T, 64>(c, a, ws, num_sms, st);
+    if (c.head_dim == 128) return launch_dim<T, 128>(c, a, ws, num_sms, st);
+    return launch_dim<T, 256>(c, a, ws, num_sms, st);
 }
 
 }  // namespace
 
-size_t kv8_attention_workspace(const Kv8 &, int, int, int, int) { return 256; }
+// Two pieces per CTA of the widest row tile.
+size_t kv8_attention_workspace(const Kv8 &c, int n, int, int, int num_sms) {
+    const int rows = 8 * (c.head_dim == 64 ? wide_tiles<64>() : c.head_dim == 128 ? wide_tiles<128>() : wide_tiles<256>());
+    return 256 + align256((size_t)(n + 1) * 8) + align256((size_t)num_sms * 2 * rows * (c.head_dim + 4) * sizeof(float));
+}
 
-cudaError_t launch_kv8_attention(const Kv8 &c, const Kv8Query &a, void *, int, cudaStream_t st) {
-    const dim3 grid((unsigned)((long long)a.n * a.q_len * a.heads));
-    if (a.dtype == TP_MLP_F32) return launch_pdl(attention_rows_kernel<float>, grid, dim3(kThreads), 0, st, c, a);
-    return launch_pdl(attention_rows_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, c, a);
+cudaError_t launch_kv8_attention(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
+    if (a.dtype == TP_MLP_F32) return launch_typed<float>(c, a, ws, num_sms, st);
+    return launch_typed<__nv_bfloat16>(c, a, ws, num_sms, st);
 }
 
 }  // namespace tpmlp
