@@ -567,6 +567,8 @@ typedef enum {
 
 /* Most sequences (or page pairs) in one call's list. */
 #define TP_MLP_KV8_MAX_LIST 1024
+/* Most queries of a sequence in one attention call. */
+#define TP_MLP_KV8_MAX_QUERIES 128
 
 /*
  * Status of the cache's calls so far: synchronises the device, stores the
@@ -674,7 +676,8 @@ int tp_mlp_kv8_append(const tp_mlp_kv8_cache *cache, int layer, const void *k, c
  *   positions  device, n ints, or NULL
  *   workspace  device, tp_mlp_kv8_attention_workspace_bytes bytes; no contents
  *              are kept between calls, but calls that overlap need their own
- * 1 <= n <= TP_MLP_KV8_MAX_LIST (0 is a no-op), 1 <= q_len <= 128, heads a
+ * 1 <= n <= TP_MLP_KV8_MAX_LIST (0 is a no-op), 1 <= q_len <=
+ * TP_MLP_KV8_MAX_QUERIES, heads a
  * multiple of kv_heads with heads / kv_heads <= 128, scale finite.
  */
 size_t tp_mlp_kv8_attention_workspace_bytes(const tp_mlp_kv8_cache *cache, int n, int q_len, int heads);

@@ -67,7 +67,7 @@ struct Kv8Query {
     void *o;
     float *maximum, *exp_sum;
 };
-size_t kv8_attention_workspace(const Kv8 &c, int n, int q_len, int heads, int num_sms);
+size_t kv8_attention_workspace(const Kv8 &c, int num_sms);
 cudaError_t launch_kv8_attention(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st);
 
 // kv8_pages.cu

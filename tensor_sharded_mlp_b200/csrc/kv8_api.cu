@@ -94,7 +94,7 @@ int check_rows(const void *p, long long rows, long long width, long long stride,
 }
 
 int attention_sizes(const Kv8 &c, int n, int q_len, int heads) {
-    if (n < 0 || n > TP_MLP_KV8_MAX_LIST || q_len < 1 || q_len > 128 || heads < 1) return TP_MLP_ERR_SHAPE;
+    if (n < 0 || n > TP_MLP_KV8_MAX_LIST || q_len < 1 || q_len > TP_MLP_KV8_MAX_QUERIES || heads < 1) return TP_MLP_ERR_SHAPE;
     if (heads % c.kv_heads != 0 || heads / c.kv_heads > 128) return TP_MLP_ERR_SHAPE;
     return TP_MLP_OK;
 }
@@ -125,7 +125,7 @@ int attention(const tp_mlp_kv8_cache *cache, int layer, const Kv8Query &a, bool 
     if ((s = check_list(a.seqs, a.n, true)) || (s = check_list(a.positions, a.n, true))) return s;
     int sms = 0;
     if ((s = sm_count(&sms))) return s;
-    const size_t need = kv8_attention_workspace(c, a.n, a.q_len, a.heads, sms);
+    const size_t need = kv8_attention_workspace(c, sms);
     if (!ws || ws_bytes < need) return TP_MLP_ERR_WORKSPACE;
     if ((s = check_dev(ws, need))) return s;
     to_layer(&c, layer);
@@ -254,7 +254,7 @@ size_t tp_mlp_kv8_attention_workspace_bytes(const tp_mlp_kv8_cache *cache, int n
         cudaGetLastError();
         sms = 148;   // B200
     }
-    return kv8_attention_workspace(c, n, q_len, heads, sms);
+    return kv8_attention_workspace(c, sms);
 }
 
 int tp_mlp_kv8_attention(const tp_mlp_kv8_cache *cache, int layer, const void *q, long long row_stride,

@@ -43,6 +43,7 @@
 // never loaded (zero-filled), a masked score is -inf before it is used, and a
 // NaN value that only some rows see is taken out of the product and put into
 // just their outputs.
+#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -54,45 +55,50 @@
 namespace tpmlp {
 namespace {
 
+#ifndef KSTAGES
+#define KSTAGES (D == 256 ? 2 : D == 128 ? 4 : 6)
+#endif
 constexpr int kStep = 16;            // tokens of one step
 constexpr float kSlack = 8.f;        // how far (base-2 logs) a score may exceed the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
-constexpr int kCombineThreads = 256;
 
-// Shared memory: [ring of every warp | first piece of every warp | prefix of the entries' steps | piece table].  A warp
-// leaves at most two pieces, at the start and at the end of its steps; the second lies in its ring, which is idle then.
+// Shared memory: [ring of every warp | first piece of every warp | scales of every ring place | prefix of the entries'
+// steps | entries | piece table].  A warp leaves at most two pieces, at the start and at the end of its steps; the second
+// lies in its ring, which is idle then.
 template <int D, int NT>
 struct Cfg {
     static constexpr int kWarps = 8;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = 8 * NT;
     static constexpr int kStage = 2 * kStep * D;                       // keys and values of one step
-    static constexpr int kStages = D == 256 ? 2 : D == 128 ? 4 : 6;
+    static constexpr int kStages = KSTAGES;
     static constexpr int kRing = kStage * kStages;
     static constexpr int kPad = D + 4;                                  // floats a piece's row takes
     static constexpr int kPiece = kRows * (kPad + 4) * 4;               // outputs, reference, sum, maximum
     static_assert(kPiece <= kRing, "the second piece lies in the ring");
-    static constexpr size_t smem(int n) { return (size_t)kWarps * (kRing + kPiece) + (n + 2) / 2 * 2 * 8 + kWarps * 2 * 4; }
+    static constexpr size_t kScaleOff = (size_t)kWarps * (kRing + kPiece);
+    static constexpr size_t kPrefixOff = kScaleOff + kWarps * kStages * 8;
+    static constexpr size_t smem(int n) { return kPrefixOff + (size_t)(n + 1) * 8 + (size_t)n * 16 + kWarps * 2 * 4; }
 };
 
-// Workspace: [header: total steps, CTAs at work | prefix, n + 1 | two pieces per CTA]
+// Workspace: [a segment to join per CTA | two pieces per CTA].  CTA i's is the segment that begins in it and goes on in
+// the next ones: {entry, unit, CTAs that share it, -}, with a count of 0 for none.
 struct Split {
-    long long *total;      // [0] steps, [1] CTAs
-    long long *prefix;
+    int4 *shared;
     float *pieces;
 };
 
 struct Entry {             // one entry of the call's list
-    int seq, len, seen;    // seen: tokens that its last query sees; seq -1: passed over
-    long long first;       // position of its query 0
+    int seq, len;          // seq -1: passed over
+    int first;             // position of its query 0, brought to [-128, len]: no token's visibility changes
+    __device__ __forceinline__ int seen(int query) const { return max(0, min(len, first + query + 1)); }
 };
 
 __device__ __forceinline__ Entry load_entry(const Kv8 &c, const Kv8Query &a, int i, int *bad) {
     Entry e;
     e.seq = kv8_seq(a.seqs, i);
-    e.len = e.seen = 0;
-    e.first = 0;
+    e.len = e.first = 0;
     if (e.seq == -1) return e;
     if ((unsigned)e.seq >= (unsigned)c.max_seqs) {
         *bad |= TP_MLP_KV8_BAD_SEQUENCE;
@@ -106,15 +112,25 @@ __device__ __forceinline__ Entry load_entry(const Kv8 &c, const Kv8Query &a, int
         e.len = 0;
         return e;
     }
-    e.first = a.positions ? (long long)a.positions[i] : (long long)e.len - a.q_len;
-    e.seen = (int)max(0LL, min((long long)e.len, e.first + a.q_len));
+    e.first = max(-TP_MLP_KV8_MAX_QUERIES, min(e.len, a.positions ? a.positions[i] : e.len - a.q_len));
     return e;
 }
 
+// a / b for a >= 0, b > 0, by the short division where it can be.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+    return a <= 0x7fffffffLL ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // --- register-level pieces ------------------------------------------------------
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool take) {
     const int bytes = take ? 16 : 0;   // 0: the 16 bytes are filled with zeros
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -122,6 +138,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
     return v;
+}
+__device__ __forceinline__ void sts64(uint32_t p, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(p), "f"(x), "f"(y) : "memory");
 }
 __device__ __forceinline__ uint2 lds64(uint32_t p) {
     uint2 v;
@@ -175,17 +194,27 @@ __device__ __forceinline__ int key_chunk(int t, int i) {
     return D == 64 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
 }
 
-// Eight query elements as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *f) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
-    f[4] = bf16lo(u.z); f[5] = bf16hi(u.z); f[6] = bf16lo(u.w); f[7] = bf16hi(u.w);
-}
-__device__ __forceinline__ void load8(const float *p, float *f) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
+// Eight query elements as loaded.
+template <typename T> struct RawQuery;
+template <> struct RawQuery<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void widen(float *f) const {
+        f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
+        f[4] = bf16lo(u.z); f[5] = bf16hi(u.z); f[6] = bf16lo(u.w); f[7] = bf16hi(u.w);
+    }
+};
+template <> struct RawQuery<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ void widen(float *f) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
 
 // Where row r (0 .. q_len * group - 1) of (entry, KV head) is in q and the outputs.
 struct RowMap {
@@ -221,6 +250,24 @@ __device__ __forceinline__ RowResult row_result(float ref, float sum, float top,
     return r;
 }
 
+// Writes a joined row of the result (one warp).
+template <typename T, int D>
+__device__ __forceinline__ void write_row(const Kv8Query &a, long long orow, float ref, float sum, float top,
+                                          const float4 (&v)[(D + 127) / 128]) {
+    const int lane = threadIdx.x & 31;
+    const RowResult res = row_result(ref, sum, top, a.maximum != nullptr);
+#pragma unroll
+    for (int x = 0; x < (D + 127) / 128; ++x) {
+        if (D == 64 && lane >= 16) continue;
+        store4(static_cast<T *>(a.o) + orow * D + 4 * (lane + 32 * x),
+               make_float4(v[x].x * res.factor, v[x].y * res.factor, v[x].z * res.factor, v[x].w * res.factor));
+    }
+    if (a.maximum && lane == 0) {
+        a.maximum[orow] = res.maximum;
+        a.exp_sum[orow] = res.exp_sum;
+    }
+}
+
 // --- the streaming kernel ----------------------------------------------------------
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
@@ -235,26 +282,36 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const int group = a.heads / c.kv_heads, rows = a.q_len * group;
     const int units_per_entry = c.kv_heads * row_tiles;
     const uint32_t ring = tc::smem_u32(smem) + warp * C::kRing;
+    const uint32_t scales = tc::smem_u32(smem) + (uint32_t)C::kScaleOff + warp * C::kStages * 8;
     auto piece_at = [&](int w, int p) {
         return reinterpret_cast<float *>(smem + (p ? (size_t)w * C::kRing : (size_t)C::kWarps * C::kRing + (size_t)w * C::kPiece));
     };
-    long long *prefix = reinterpret_cast<long long *>(smem + (size_t)C::kWarps * (C::kRing + C::kPiece));
-    int *piece_seg = reinterpret_cast<int *>(prefix + (n + 2) / 2 * 2);
+    long long *prefix = reinterpret_cast<long long *>(smem + C::kPrefixOff);
+    int *e_seq = reinterpret_cast<int *>(prefix + n + 1), *e_len = e_seq + n, *e_first = e_len + n;
+    int *e_steps = e_first + n;       // of one segment of the entry
+    int *piece_seg = e_steps + n;
     __shared__ long long scan_part[C::kWarps];
 
     pdl_allow_dependents();
     pdl_wait_previous();
 
-    // 1. steps of every entry, and their prefix sums
+    // 1. the entries, the steps of each, and their prefix sums
     {
-        constexpr int kPer = kMaxList / C::kThreads;
+        constexpr int kPer = (kMaxList + C::kThreads - 1) / C::kThreads;
         long long mine[kPer], sum = 0;
         int bad = 0;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             const int i = tid * kPer + u;
             mine[u] = sum;
-            if (i < n) sum += (long long)((load_entry(c, a, i, &bad).seen + kStep - 1) / kStep) * units_per_entry;
+            if (i < n) {
+                const Entry en = load_entry(c, a, i, &bad);
+                e_seq[i] = en.seq;
+                e_len[i] = en.len;
+                e_first[i] = en.first;
+                e_steps[i] = (en.seen(a.q_len - 1) + kStep - 1) / kStep;
+                sum += (long long)e_steps[i] * units_per_entry;
+            }
         }
         if (bad && blockIdx.x == 0) kv8_flag(c, bad);
         long long x = sum;
@@ -271,25 +328,37 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
         for (int u = 0; u < kPer; ++u)
             if (tid * kPer + u <= n) prefix[tid * kPer + u] = base + mine[u];
-        if (n == kMaxList && tid == C::kThreads - 1) prefix[n] = base + sum;
+        if (n == kPer * C::kThreads && tid == C::kThreads - 1) prefix[n] = base + sum;
         if (lane < 2) piece_seg[warp * 2 + lane] = -1;
         __syncthreads();
     }
     const long long total = prefix[n];
-    const long long ctas = max(1LL, min((long long)gridDim.x, (total + C::kWarps - 1) / C::kWarps));
-    if (blockIdx.x == 0) {
-        for (int i = tid; i <= n; i += C::kThreads) ws.prefix[i] = prefix[i];
-        if (tid == 0) {
-            ws.total[0] = total;
-            ws.total[1] = ctas;
-        }
+    const int ctas = (int)max(1LL, min((long long)gridDim.x, (total + C::kWarps - 1) / C::kWarps));
+    // CTA i takes steps first_step(i) .. first_step(i + 1) - 1: equal shares, the first `extra` one step more
+    const long long share = quotient(total, ctas);
+    const int extra = (int)(total - share * ctas);
+    auto first_step = [&](int i) { return share * i + min(i, extra); };
+    // entries that see nothing: their rows are written here (a few, if any)
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+        if (e_steps[i] > 0 || e_seq[i] < 0) continue;
+        const long long row0 = (long long)i * a.q_len * a.heads, row_n = (long long)a.q_len * a.heads;
+        for (long long x = tid; x < row_n * (D / 4); x += C::kThreads)
+            store4(static_cast<T *>(a.o) + row0 * D + 4 * x, make_float4(0.f, 0.f, 0.f, 0.f));
+        if (a.maximum)
+            for (long long x = tid; x < row_n; x += C::kThreads) {
+                a.maximum[row0 + x] = -INFINITY;
+                a.exp_sum[row0 + x] = 0.f;
+            }
     }
-    if (blockIdx.x >= ctas || total == 0) return;
-    const long long c0 = total * blockIdx.x / ctas, c1 = total * (blockIdx.x + 1) / ctas;
+    if (blockIdx.x >= ctas || total == 0) {
+        if (tid == 0) ws.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    const long long c0 = first_step(blockIdx.x), c1 = first_step(blockIdx.x + 1);
     const long long w0 = c0 + (c1 - c0) * warp / C::kWarps, w1 = c0 + (c1 - c0) * (warp + 1) / C::kWarps;
 
-    // 2. this warp's steps, segment by segment
-    int e = 0;
+    // 2. this warp's steps, segment by segment.  The loads run kStages - 1 steps ahead of the products, across segments.
+    int e = 0, unit = 0, n_pieces = 0;
     if (w0 < w1) {   // the entry that holds step w0: the last with prefix <= w0
         int lo = 0, hi = n;
         while (hi - lo > 1) {
@@ -299,139 +368,213 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         e = lo;
     }
-    int n_pieces = 0;
-    for (long long at = w0; at < w1;) {
-        while (prefix[e + 1] <= at) ++e;
-        const long long entry0 = prefix[e];
-        const int steps = (int)((prefix[e + 1] - entry0) / units_per_entry);
-        const int unit = (int)((at - entry0) / steps);
-        const long long seg0 = entry0 + (long long)unit * steps;
-        const int s0 = (int)(at - seg0), s1 = (int)min((long long)steps, w1 - seg0);
-        at = seg0 + s1;
-        const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
-        int bad = 0;
-        const Entry en = load_entry(c, a, e, &bad);
-        const RowMap map = {e, kv_head, group, a.q_len, a.heads};
+    const int page_steps = c.page_shift - 4;            // log2(steps of a page)
 
-        // queries: row g of each n-tile, this thread's columns of every k-step
-        uint32_t q[kParts][NT][kKs][2];
-        float fac[NT][2];
-        int limit[NT][2];      // tokens that the column's row sees
+    // The loading side: its segment (first step lseg; steps ls .. lend - 1 are this warp's), and the pages of its batch
+    // of 32 (lane x holds the x-th); the next batch's page numbers (of this segment, or the next one's first) are loaded
+    // while this one is in use.  key_ptr and scale_ptr move on from step to step within a page.
+    int le = e, lunit = 0, ls = 0, lend = 0, lbatch = 0, lpage = 0, npage = 0, llen = 0, lhead = 0;
+    long long lseg = w1;
+    const uint8_t *key_ptr = nullptr;
+    const float *scale_ptr = nullptr;
+    const long long to_values = c.v - c.k;
+    uint32_t chunk[D / 32];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = (tile * NT + nt) * 8 + g;
-            const bool have = r < rows;
-            const int rr = have ? r : 0, j = map.query(rr);
-            const T *src = static_cast<const T *>(a.q) + ((long long)e * a.q_len + j) * a.row_stride +
-                           (long long)(kv_head * group + rr - j * group) * D;
-            float f[D / 4];
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                load8(src + key_chunk<D>(t, i) * 16, f + 16 * i);
-                load8(src + key_chunk<D>(t, i) * 16 + 8, f + 16 * i + 8);
-            }
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(f[i]));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-            ex = ex > 127 ? 0 : max(ex, -126);   // an infinite row stays as it is
-            const float scale_down = ex == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - ex) << 23);   // 2^-ex
-#pragma unroll
-            for (int k = 0; k < kKs; ++k) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float v0 = have ? f[4 * k + 2 * x] * scale_down : 0.f;
-                    const float v1 = have ? f[4 * k + 2 * x + 1] * scale_down : 0.f;
-                    q[0][nt][k][x] = f16x2(v0, v1);
-                    if (kExact) {
-                        const float2 h = widen_f16x2(q[0][nt][k][x]);
-                        q[kParts - 1][nt][k][x] = f16x2(v0 - h.x, v1 - h.y);
-                    }
-                }
-            }
-            const float up = have ? ldexpf(a.scale * kLog2e, ex) : 0.f;
-            const int lim = have ? (int)max(0LL, min((long long)en.len, en.first + j + 1)) : 0x7fffffff;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                fac[nt][x] = __shfl_sync(0xffffffffu, up, (2 * t + x) * 4);
-                limit[nt][x] = __shfl_sync(0xffffffffu, lim, (2 * t + x) * 4);
-            }
+    for (int i = 0; i < D / 32; ++i) chunk[i] = chunk_at<D>((i * 32 + lane) / (D / 16), (i * 32 + lane) % (D / 16));
+    auto load_pages = [&](int i, int b) {
+        const int x = b * 32 + lane;
+        return x < c.pages_of(e_len[i]) ? c.table[(long long)e_seq[i] * c.max_pages + x] : -1;
+    };
+    auto take_batch = [&]() {   // npage becomes the batch in use
+        const bool ok = (unsigned)npage < (unsigned)c.num_pages;
+        if (!ok && lbatch * 32 + lane <= (lend - 1) >> page_steps) kv8_flag(c, TP_MLP_KV8_BAD_PAGE);
+        lpage = ok ? npage : -1;
+        if ((lend - 1) >> (page_steps + 5) > lbatch) {
+            npage = load_pages(le, lbatch + 1);
+        } else if (lseg + lend < w1) {
+            int i = le;
+            if (lunit + 1 == units_per_entry)
+                do ++i;
+                while (e_steps[i] == 0);
+            npage = load_pages(i, 0);
         }
-        // steps below `plain` need no mask: the tile's first row sees the fewest tokens
-        const int least = (int)max(0LL, min((long long)en.len, en.first + map.query(tile * C::kRows) + 1));
-        const int plain = least / kStep;
-
-        float o[NT][kMt][4], ref[NT][2], sum[NT][2], top[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int m = 0; m < kMt; ++m)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[nt][m][k] = 0.f;
-            ref[nt][0] = ref[nt][1] = top[nt][0] = top[nt][1] = -INFINITY;
-            sum[nt][0] = sum[nt][1] = 0.f;
-        }
-
-        // pages come 32 at a time: lane x holds the x-th one's number and scales.  The loads run ahead of the
-        // products by fewer than 32 steps, so the products are in this batch or in the one before.
-        const int *row = c.table + (long long)en.seq * c.max_pages;
-        const int page_steps = c.page_shift - 4;            // log2(steps of a page)
-        const int n_pages = c.pages_of(en.len);
-        int batch = -1, page = 0;
-        float ks = 0.f, vs = 0.f, ks_before = 0.f, vs_before = 0.f;
-        auto fetch = [&](int s, int slot) {
-            const int nth = s >> page_steps;
-            if ((nth >> 5) != batch) {
-                batch = nth >> 5;
-                ks_before = ks;
-                vs_before = vs;
-                const int mine = batch * 32 + lane;
-                page = mine < n_pages ? row[mine] : 0;
-                const bool ok = (unsigned)page < (unsigned)c.num_pages;
-                if (!ok && mine <= (s1 - 1) >> page_steps) kv8_flag(c, TP_MLP_KV8_BAD_PAGE);
-                page = ok ? page : -1;
-                const long long head = (long long)(ok ? page : 0) * c.kv_heads + kv_head;
-                ks = c.k_scale[head];
-                vs = ok ? c.v_scale[head] : -1.f;           // negative: not a page of the pool
+    };
+    if (w0 < w1) {
+        const int steps = e_steps[e];
+        unit = lunit = (int)quotient(w0 - prefix[e], steps);
+        lhead = lunit / row_tiles;
+        llen = e_len[e];
+        lseg = prefix[e] + (long long)lunit * steps;
+        ls = (int)(w0 - lseg);
+        lend = (int)min((long long)steps, w1 - lseg);
+        lbatch = ls >> (page_steps + 5);
+        npage = load_pages(e, lbatch);
+    }
+    bool turn_page = true;
+    auto fetch = [&](int place) {
+        if (ls == lend) {                                  // the next segment
+            lseg += lend;
+            if (lseg >= w1) {
+                lend = ls = 0;
+                return;
             }
-            const int p = __shfl_sync(0xffffffffu, page, nth & 31);
-            const long long off = (((long long)(p < 0 ? 0 : p) * c.kv_heads + kv_head) * c.page_size +
-                                   ((s * kStep) & (c.page_size - 1))) * D;
-            const int live = p < 0 ? 0 : en.len - s * kStep;   // rows behind the end are zeros
-            const uint32_t dst = ring + slot * C::kStage;
+            if (++lunit == units_per_entry) {
+                lunit = 0;
+                do ++le;
+                while (e_steps[le] == 0);
+                llen = e_len[le];
+            }
+            lhead = lunit / row_tiles;
+            ls = 0;
+            lend = (int)min((long long)e_steps[le], w1 - lseg);
+            lbatch = 0;
+            take_batch();
+            turn_page = true;
+        } else if (ls >> (page_steps + 5) != lbatch) {
+            lbatch = ls >> (page_steps + 5);
+            take_batch();
+        }
+        if (turn_page) {
+            const int p = __shfl_sync(0xffffffffu, lpage, (ls >> page_steps) & 31);
+            const long long head = (long long)(p < 0 ? 0 : p) * c.kv_heads + lhead;
+            key_ptr = p < 0 ? nullptr : c.k + (head * c.page_size + ((ls * kStep) & (c.page_size - 1))) * D + 16 * lane;
+            scale_ptr = (lane ? c.v_scale : c.k_scale) + head;
+        }
+        const uint32_t dst = ring + place * C::kStage;
+        const int live = key_ptr ? llen - ls * kStep : 0;      // rows behind the end are zeros
+        if (live >= kStep) {
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const int x = i * 32 + lane, r = x / (D / 16), ch = x % (D / 16);
-                cp_async16(dst + chunk_at<D>(r, ch), c.k + off + 16 * x, r < live);
-                cp_async16(dst + kStep * D + chunk_at<D>(r, ch), c.v + off + 16 * x, r < live);
+                cp_async16(dst + chunk[i], key_ptr + 512 * i);
+                cp_async16(dst + kStep * D + chunk[i], key_ptr + to_values + 512 * i);
             }
-        };
-        int slot = 0;
+        } else {
+            const uint8_t *src = key_ptr ? key_ptr : c.k;
 #pragma unroll
-        for (int i = 0; i < C::kStages - 1; ++i) {
-            if (s0 + i < s1) fetch(s0 + i, i);
-            cp_commit();
+            for (int i = 0; i < D / 32; ++i) {
+                const bool take = (i * 32 + lane) / (D / 16) < live;
+                cp_async16_or_zero(dst + chunk[i], src + 512 * i, take);
+                cp_async16_or_zero(dst + kStep * D + chunk[i], src + to_values + 512 * i, take);
+            }
         }
-        for (int s = s0; s < s1; ++s) {
+        if (!key_ptr) {
+            if (lane == 0) sts64(scales + place * 8, 0.f, -1.f);   // negative: not a page of the pool
+        } else if (lane < 2) {
+            cp_async4(scales + place * 8 + lane * 4, scale_ptr);
+        }
+        ++ls;
+        turn_page = (ls & ((1 << page_steps) - 1)) == 0;
+        if (key_ptr) key_ptr += kStep * D;
+    };
+    // The products' side: segment (e, unit), of which this warp has steps s0 .. s1 - 1 and is at s.
+    constexpr bool kAhead = NT == 1 && !kExact;   // queries are loaded ahead where the registers hold them
+    RawQuery<T> raw[NT][D / 32];
+    auto load_queries = [&]() {
+        const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = (tile * NT + nt) * 8 + g, rr = r < rows ? r : 0, j = rr / group;
+            const T *src = static_cast<const T *>(a.q) + ((long long)e * a.q_len + j) * a.row_stride +
+                           (long long)(kv_head * group + rr - j * group) * D;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                raw[nt][2 * i].load(src + key_chunk<D>(t, i) * 16);
+                raw[nt][2 * i + 1].load(src + key_chunk<D>(t, i) * 16 + 8);
+            }
+        }
+    };
+    uint32_t q[kParts][NT][kKs][2];
+    float fac[NT][2];
+    int limit[NT][2];      // tokens that the column's row sees
+    int plain = 0;
+    float o[NT][kMt][4], ref[NT][2], sum[NT][2], top[NT][2];
+    int steps = 0, s0 = 0, s1 = 0, s = 0;
+    if (w0 < w1) {
+        if (kAhead) load_queries();
+        steps = e_steps[e];
+        s = s0 = ls;
+        s1 = lend;
+        take_batch();
+    }
+    int place = 0;
+#pragma unroll 1
+    for (int i = 0; i < C::kStages - 1; ++i) {
+        fetch(i);
+        cp_commit();
+    }
+    for (long long at = w0; at < w1;) {
+        {
+            const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
+            if (!kAhead) load_queries();
+            const Entry en = {e_seq[e], e_len[e], e_first[e]};
+            const RowMap map = {e, kv_head, group, a.q_len, a.heads};
+            // queries: row g of each n-tile, this thread's columns of every k-step
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = (tile * NT + nt) * 8 + g;
+                const bool have = r < rows;
+                float f[D / 4];
+                float amax = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) raw[nt][i].widen(f + 8 * i);
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(f[i]));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+                ex = ex > 127 ? 0 : max(ex, -126);   // an infinite row stays as it is
+                const float down = ex == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - ex) << 23);   // 2^-ex
+#pragma unroll
+                for (int k = 0; k < kKs; ++k) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float v0 = have ? f[4 * k + 2 * x] * down : 0.f;
+                        const float v1 = have ? f[4 * k + 2 * x + 1] * down : 0.f;
+                        q[0][nt][k][x] = f16x2(v0, v1);
+                        if (kExact) {
+                            const float2 h = widen_f16x2(q[0][nt][k][x]);
+                            q[kParts - 1][nt][k][x] = f16x2(v0 - h.x, v1 - h.y);
+                        }
+                    }
+                }
+                const float up = have ? ldexpf(a.scale * kLog2e, ex) : 0.f;
+                const int lim = have ? en.seen(map.query(r)) : 0x7fffffff;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    fac[nt][x] = __shfl_sync(0xffffffffu, up, (2 * t + x) * 4);
+                    limit[nt][x] = __shfl_sync(0xffffffffu, lim, (2 * t + x) * 4);
+                }
+            }
+            // steps below `plain` need no mask: the tile's first row sees the fewest tokens
+            plain = en.seen(map.query(tile * C::kRows)) / kStep;
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int m = 0; m < kMt; ++m)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[nt][m][k] = 0.f;
+                ref[nt][0] = ref[nt][1] = -FLT_MAX;   // finite: a masked score minus it is -inf, never NaN
+                top[nt][0] = top[nt][1] = -INFINITY;
+                sum[nt][0] = sum[nt][1] = 0.f;
+            }
+        }
+        for (; s < s1; ++s) {
             cp_wait<C::kStages - 2>();
             __syncwarp();
-            // (every lane is done with the slot that this fetch refills: it was read a step ago)
-            if (s + C::kStages - 1 < s1) fetch(s + C::kStages - 1, slot == 0 ? C::kStages - 1 : slot - 1);
+            // (every lane is done with the place that this fetch refills: it was read a step ago)
+            fetch(place == 0 ? C::kStages - 1 : place - 1);
             cp_commit();
-            const uint32_t keys = ring + slot * C::kStage, vals = keys + kStep * D;
-            slot = slot + 1 == C::kStages ? 0 : slot + 1;
-            const int nth = s >> page_steps;
-            const bool current = (nth >> 5) == batch;
-            const float kscale = __shfl_sync(0xffffffffu, current ? ks : ks_before, nth & 31);
-            const float vscale = __shfl_sync(0xffffffffu, current ? vs : vs_before, nth & 31);
-            if (vscale < 0.f) continue;                     // none of this page's tokens is seen
-
+            const uint32_t keys = ring + place * C::kStage, vals = keys + kStep * D;
+            const uint2 pair = lds64(scales + place * 8);
+            const float kscale = __uint_as_float(pair.x), vscale = __uint_as_float(pair.y);
+            place = place + 1 == C::kStages ? 0 : place + 1;
+            if (vscale < 0.f) continue;                     // not a page of the pool: nothing is seen
             // scores: 16 tokens x 8 rows a tile
-            float sc[NT][4];
+            float sc[NT][4], sc2[NT][4];      // two sums: half as long a chain of dependent products
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[nt][k] = sc2[nt][k] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 const uint4 lo4 = lds128(keys + chunk_at<D>(g, key_chunk<D>(t, i)));
@@ -446,7 +589,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int pt = 0; pt < kParts; ++pt)
-                            mma(sc[nt], a0, a1, a2, a3, q[pt][nt][4 * i + w][0], q[pt][nt][4 * i + w][1]);
+                            mma(w & 1 ? sc2[nt] : sc[nt], a0, a1, a2, a3, q[pt][nt][4 * i + w][0], q[pt][nt][4 * i + w][1]);
                 }
             }
             // base-2 scores; the binade above the value scale
@@ -458,7 +601,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float x = sc[nt][k] * (fac[nt][k & 1] * kscale);
+                    float x = (sc[nt][k] + sc2[nt][k]) * (fac[nt][k & 1] * kscale);
                     if (masked && s * kStep + g + 8 * (k >> 1) >= limit[nt][k & 1]) x = -INFINITY;
                     sc[nt][k] = x;
                     rise |= x + vlog > ref[nt][k & 1] + kSlack;
@@ -491,8 +634,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 float p[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float r = ref[nt][k & 1];
-                    p[k] = exp2_fast(sc[nt][k] - (r == -INFINITY ? 0.f : r));
+                    p[k] = exp2_fast(sc[nt][k] - ref[nt][k & 1]);
                     sum[nt][k & 1] += p[k];
                     p[k] *= vscale;
                 }
@@ -583,8 +725,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                             mma(o[nt][2 * i + h], a0, a1, a2, a3, w[pt][nt][0], w[pt][nt][1]);
                 }
         }
-        cp_wait<0>();
-        __syncwarp();   // the ring is free for the next segment
+        at += s1 - s0;
+
+        // the segment's end: its rows, or a piece of them
+        const int done_e = e, done_unit = unit;
+        const bool whole = s0 == 0 && s1 == steps;
+        if (at < w1) {
+            if (++unit == units_per_entry) {
+                unit = 0;
+                do ++e;
+                while (e_steps[e] == 0);
+                steps = e_steps[e];
+            }
+            s = s0 = 0;
+            s1 = (int)min((long long)steps, w1 - at);
+            if (kAhead) load_queries();
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -594,10 +750,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     sum[nt][x] += __shfl_xor_sync(0xffffffffu, sum[nt][x], m);
                     top[nt][x] = fmaxf(top[nt][x], __shfl_xor_sync(0xffffffffu, top[nt][x], m));
                 }
-
-        // 3. a whole segment is written; a piece of one goes to shared memory.  The thread's column of output
-        // product 2 i + h, element pair (x, x + 2), is column(i) + 2 h (+ 1).
-        const bool whole = s0 == 0 && s1 == steps;
+        __syncwarp();   // (a second piece overwrites the ring)
+        const int kv_head = done_unit / row_tiles, tile = done_unit - kv_head * row_tiles;
+        const RowMap map = {done_e, kv_head, group, a.q_len, a.heads};
+        // (a whole segment is written, a piece of one goes to shared memory.  The thread's column of output
+        // product 2 i + h, element pair (x, x + 2), is column(i) + 2 h (+ 1).)
         float *piece = piece_at(warp, n_pieces);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -632,151 +789,187 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 }
             }
         if (!whole) {
-            if (lane == 0) piece_seg[warp * 2 + n_pieces] = e * units_per_entry + unit;
+            if (lane == 0) piece_seg[warp * 2 + n_pieces] = done_e * units_per_entry + done_unit;
             ++n_pieces;
         }
     }
     __syncthreads();
 
-    // 4. join the pieces of each segment, in order; pieces that other CTAs share go to the workspace
-    for (int first = 0; first < 2 * C::kWarps;) {
-        const int seg = piece_seg[first];
-        int last = first + 1;   // a segment's pieces are neighbours but for unused places
-        if (seg < 0) {
-            first = last;
-            continue;
+    // 3. join the pieces of each segment, in order; those of a segment that other CTAs share go to the workspace.  A warp
+    // takes a row: lane p first works out piece p's weight in its segment, then the lanes are columns.
+    constexpr int kPieces = 2 * C::kWarps;
+    static_assert(kPieces <= 32, "a lane per piece");
+    constexpr int kCols = (D + 127) / 128;                  // float4 columns of a lane
+    const int seg = lane < kPieces ? piece_seg[lane] : -1;
+    for (int in_tile = warp; in_tile < C::kRows; in_tile += C::kWarps) {
+        float4 stat = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (seg >= 0) stat = *reinterpret_cast<const float4 *>(piece_at(lane >> 1, lane & 1) + C::kRows * C::kPad + in_tile * 4);
+        float r = stat.x, tp = stat.z, l = 0.f;
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const bool same = __shfl_sync(0xffffffffu, seg, p) == seg;
+            const float x = __shfl_sync(0xffffffffu, stat.x, p), z = __shfl_sync(0xffffffffu, stat.z, p);
+            r = same ? fmaxf(r, x) : r;
+            tp = same ? fmaxf(tp, z) : tp;
         }
-        while (last < 2 * C::kWarps && (piece_seg[last] == seg || piece_seg[last] < 0)) ++last;
-        const int se = seg / units_per_entry, unit = seg - se * units_per_entry;
-        const long long entry0 = prefix[se];
-        const int steps = (int)((prefix[se + 1] - entry0) / units_per_entry);
-        const long long seg0 = entry0 + (long long)unit * steps;
-        const bool whole = seg0 >= c0 && seg0 + steps <= c1;
-        const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
-        const RowMap map = {se, kv_head, group, a.q_len, a.heads};
-        float *out = ws.pieces + ((size_t)blockIdx.x * 2 + (seg0 < c0 ? 0 : 1)) * (C::kRows * (D + 4));
-        for (int x = tid; x < C::kRows * (D / 4); x += C::kThreads) {
-            const int in_tile = x / (D / 4), col = (x - in_tile * (D / 4)) * 4;
-            float r = -INFINITY, tp = -INFINITY;
-            for (int p = first; p < last; ++p) {
-                if (piece_seg[p] < 0) continue;
-                const float *stat = piece_at(p >> 1, p & 1) + C::kRows * C::kPad + in_tile * 4;
-                r = fmaxf(r, stat[0]);
-                tp = fmaxf(tp, stat[2]);
-            }
-            float l = 0.f;
-            float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p = first; p < last; ++p) {
-                if (piece_seg[p] < 0) continue;
-                const float *pc = piece_at(p >> 1, p & 1);
-                const float *stat = pc + C::kRows * C::kPad + in_tile * 4;
-                const float f = stat[0] == r ? 1.f : exp2f(stat[0] - r);   // (-inf twice is 1, on sums of 0)
-                l += stat[1] * f;
-                const float4 y = *reinterpret_cast<const float4 *>(pc + in_tile * C::kPad + col);
-                v4.x += y.x * f;
-                v4.y += y.y * f;
-                v4.z += y.z * f;
-                v4.w += y.w * f;
-            }
-            if (whole) {
-                const int rr = tile * C::kRows + in_tile;
-                if (rr < rows) {
-                    const long long orow = map.out_row(rr);
-                    const RowResult res = row_result(r, l, tp, a.maximum != nullptr);
-                    store4(static_cast<T *>(a.o) + orow * D + col,
-                           make_float4(v4.x * res.factor, v4.y * res.factor, v4.z * res.factor, v4.w * res.factor));
-                    if (a.maximum && col == 0) {
-                        a.maximum[orow] = res.maximum;
-                        a.exp_sum[orow] = res.exp_sum;
-                    }
+        const float f = seg < 0 ? 0.f : stat.x == r ? 1.f : exp2f(stat.x - r);
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const bool same = __shfl_sync(0xffffffffu, seg, p) == seg;
+            const float y = __shfl_sync(0xffffffffu, stat.y * f, p);
+            l += same ? y : 0.f;
+        }
+        float4 v[kCols];
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < kPieces; ++p) {
+            const int sg = piece_seg[p];
+            if (sg < 0) continue;
+            const float w = __shfl_sync(0xffffffffu, f, p);
+            const float *pc = piece_at(p >> 1, p & 1) + in_tile * C::kPad + 4 * lane;
+#pragma unroll
+            for (int x = 0; x < kCols; ++x)
+                if (D != 64 || lane < 16) {
+                    const float4 y = *reinterpret_cast<const float4 *>(pc + 128 * x);
+                    v[x].x += y.x * w;
+                    v[x].y += y.y * w;
+                    v[x].z += y.z * w;
+                    v[x].w += y.w * w;
                 }
+            int after = p + 1;   // the segment's last piece?
+            while (after < kPieces && piece_seg[after] < 0) ++after;
+            if (after < kPieces && piece_seg[after] == sg) continue;
+            const float ref_p = __shfl_sync(0xffffffffu, r, p), sum_p = __shfl_sync(0xffffffffu, l, p);
+            const float top_p = __shfl_sync(0xffffffffu, tp, p);
+            const int se = sg / units_per_entry, su = sg - se * units_per_entry, n_steps = e_steps[se];
+            const long long seg0 = prefix[se] + (long long)su * n_steps;
+            if (seg0 >= c0 && seg0 + n_steps <= c1) {
+                const int kv_head = su / row_tiles, tile = su - kv_head * row_tiles, row = tile * C::kRows + in_tile;
+                const RowMap map = {se, kv_head, group, a.q_len, a.heads};
+                if (row < rows) write_row<T, D>(a, map.out_row(row), ref_p, sum_p, top_p, v);
             } else {
-                *reinterpret_cast<float4 *>(out + in_tile * D + col) = v4;
-                if (col == 0) *reinterpret_cast<float4 *>(out + C::kRows * D + in_tile * 4) = make_float4(r, l, tp, 0.f);
+                float *out = ws.pieces + ((size_t)blockIdx.x * 2 + (seg0 < c0 ? 0 : 1)) * (C::kRows * (D + 4));
+#pragma unroll
+                for (int x = 0; x < kCols; ++x)
+                    if (D != 64 || lane < 16) *reinterpret_cast<float4 *>(out + in_tile * D + 4 * (lane + 32 * x)) = v[x];
+                if (lane == 0) *reinterpret_cast<float4 *>(out + C::kRows * D + in_tile * 4) = make_float4(ref_p, sum_p, top_p, 0.f);
             }
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        first = last;
+    }
+    // the segment that goes on in the next CTAs, if it began in this one
+    if (tid == 0) {
+        int4 d = make_int4(0, 0, 0, 0);
+        int lo = 0, hi = n;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] < c1) lo = mid;
+            else hi = mid;
+        }
+        // (the last entry that begins before c1: it holds step c1 - 1)
+        const int n_steps = e_steps[lo], su = (int)quotient(c1 - 1 - prefix[lo], n_steps);
+        const long long seg0 = prefix[lo] + (long long)su * n_steps, seg1 = seg0 + n_steps;
+        if (seg0 >= c0 && seg1 > c1) {
+            int last = blockIdx.x + 1;
+            while (first_step(last + 1) < seg1) ++last;
+            d = make_int4(lo, su, last - (int)blockIdx.x + 1, 0);
+        }
+        ws.shared[blockIdx.x] = d;
     }
 }
 
-// Joins the pieces of the segments that several CTAs share, and writes the rows of entries that see nothing.  One CTA
-// per segment.
+// Joins the pieces of the segments that several CTAs share.  kJoinWarps warps take a row: warp w the pieces w, w +
+// kJoinWarps, ...; their sums meet in shared memory.
+constexpr int kJoinWarps = 4, kJoinRows = 2;
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kCombineThreads)
+__global__ void __launch_bounds__(kJoinWarps * kJoinRows * 32)
     combine_kernel(Kv8 c, Kv8Query a, Split ws, int row_tiles) {
     using C = Cfg<D, NT>;
+    constexpr int kCols = (D + 127) / 128;
+    __shared__ float4 part[kJoinRows][kJoinWarps][kCols * 32];
+    __shared__ float4 part_stat[kJoinRows][kJoinWarps];
     pdl_allow_dependents();
     pdl_wait_previous();
-    const int units_per_entry = c.kv_heads * row_tiles;
-    const int e = blockIdx.x / units_per_entry, unit = blockIdx.x - e * units_per_entry;
-    const int group = a.heads / c.kv_heads, rows = a.q_len * group;
-    const long long entry0 = ws.prefix[e], total = ws.total[0], ctas = ws.total[1];
-    const int steps = (int)((ws.prefix[e + 1] - entry0) / units_per_entry);
-    long long from = 0, to = -1;
-    if (steps > 0) {
-        const long long seg0 = entry0 + (long long)unit * steps;
-        from = ((seg0 + 1) * ctas - 1) / total;               // the CTA that holds a step x: total*cta/ctas <= x
-        to = ((seg0 + steps) * ctas - 1) / total;
-        if (from == to) return;                                // joined there
-    } else {
-        int bad = 0;
-        if (load_entry(c, a, e, &bad).seq < 0) return;         // its rows stay as they were
+    const int4 d = ws.shared[blockIdx.x];
+    const int count = d.z;
+    if (count == 0) return;
+    const int kv_head = d.y / row_tiles, tile = d.y - kv_head * row_tiles;
+    const RowMap map = {d.x, kv_head, a.heads / c.kv_heads, a.q_len, a.heads};
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, my_row = warp / kJoinWarps, w = warp % kJoinWarps;
+    const int in_tile = blockIdx.y * kJoinRows + my_row, r = tile * C::kRows + in_tile;
+    float ref = -INFINITY, sum = 0.f, top = -INFINITY;
+    float4 v[kCols];
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = w; p < count; p += kJoinWarps) {
+        const float *pc = ws.pieces + ((size_t)(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * (C::kRows * (D + 4));
+        const float4 stat = *reinterpret_cast<const float4 *>(pc + C::kRows * D + in_tile * 4);
+        const float m = fmaxf(ref, stat.x);
+        const float f0 = ref == m ? 1.f : exp2f(ref - m), f1 = stat.x == m ? 1.f : exp2f(stat.x - m);
+        ref = m;
+        top = fmaxf(top, stat.z);
+        sum = sum * f0 + stat.y * f1;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x)
+            if (D != 64 || lane < 16) {
+                const float4 y = *reinterpret_cast<const float4 *>(pc + in_tile * D + 4 * (lane + 32 * x));
+                v[x].x = v[x].x * f0 + y.x * f1;
+                v[x].y = v[x].y * f0 + y.y * f1;
+                v[x].z = v[x].z * f0 + y.z * f1;
+                v[x].w = v[x].w * f0 + y.w * f1;
+            }
     }
-    const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
-    const RowMap map = {e, kv_head, group, a.q_len, a.heads};
-    for (int x = threadIdx.x; x < C::kRows * (D / 4); x += kCombineThreads) {
-        const int in_tile = x / (D / 4), col = (x - in_tile * (D / 4)) * 4, rr = tile * C::kRows + in_tile;
-        if (rr >= rows) continue;
-        float r = -INFINITY, tp = -INFINITY, l = 0.f;
-        for (long long p = from; p <= to; ++p) {
-            const float *stat = ws.pieces + ((size_t)p * 2 + (p == from ? 1 : 0)) * (C::kRows * (D + 4)) + C::kRows * D;
-            r = fmaxf(r, stat[in_tile * 4]);
-            tp = fmaxf(tp, stat[in_tile * 4 + 2]);
-        }
-        float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (long long p = from; p <= to; ++p) {
-            const float *pc = ws.pieces + ((size_t)p * 2 + (p == from ? 1 : 0)) * (C::kRows * (D + 4));
-            const float4 stat = *reinterpret_cast<const float4 *>(pc + C::kRows * D + in_tile * 4);
-            const float4 y = *reinterpret_cast<const float4 *>(pc + in_tile * D + col);
-            const float f = stat.x == r ? 1.f : exp2f(stat.x - r);
-            l += stat.y * f;
-            v4.x += y.x * f;
-            v4.y += y.y * f;
-            v4.z += y.z * f;
-            v4.w += y.w * f;
-        }
-        const long long orow = map.out_row(rr);
-        const RowResult res = row_result(r, l, tp, a.maximum != nullptr);
-        store4(static_cast<T *>(a.o) + orow * D + col,
-               make_float4(v4.x * res.factor, v4.y * res.factor, v4.z * res.factor, v4.w * res.factor));
-        if (a.maximum && col == 0) {
-            a.maximum[orow] = res.maximum;
-            a.exp_sum[orow] = res.exp_sum;
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) part[my_row][w][lane + 32 * x] = v[x];
+    if (lane == 0) part_stat[my_row][w] = make_float4(ref, sum, top, 0.f);
+    __syncthreads();
+    if (w != 0 || r >= a.q_len * map.group) return;
+    float m = ref;
+#pragma unroll
+    for (int p = 1; p < kJoinWarps; ++p) {
+        m = fmaxf(m, part_stat[my_row][p].x);
+        top = fmaxf(top, part_stat[my_row][p].z);
+    }
+    sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < kJoinWarps; ++p) {
+        const float4 stat = part_stat[my_row][p];
+        const float f = stat.x == m ? 1.f : exp2f(stat.x - m);
+        sum += stat.y * f;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) {
+            const float4 y = part[my_row][p][lane + 32 * x];
+            v[x].x += y.x * f;
+            v[x].y += y.y * f;
+            v[x].z += y.z * f;
+            v[x].w += y.w * f;
         }
     }
+    write_row<T, D>(a, map.out_row(r), m, sum, top, v);
 }
 
-Split split_of(void *ws, int n) {
+Split split_of(void *ws, int num_sms) {
     char *p = static_cast<char *>(ws);
-    Split s;
-    s.total = reinterpret_cast<long long *>(p);
-    s.prefix = reinterpret_cast<long long *>(p + 256);
-    s.pieces = reinterpret_cast<float *>(p + 256 + align256((size_t)(n + 1) * 8));
-    return s;
+    return Split{reinterpret_cast<int4 *>(p), reinterpret_cast<float *>(p + align256((size_t)num_sms * sizeof(int4)))};
 }
 
 template <typename T, int D, int NT>
 cudaError_t launch_tile(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
     using C = Cfg<D, NT>;
     const int rows = a.q_len * (a.heads / c.kv_heads), row_tiles = (rows + C::kRows - 1) / C::kRows;
-    const Split s = split_of(ws, a.n);
+    const Split s = split_of(ws, num_sms);
     auto kern = attention_kernel<T, D, NT>;
     cudaError_t e = ensure_smem_attr(kern, C::smem(kMaxList));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)num_sms), dim3(C::kThreads), C::smem(a.n), st, c, a, s, row_tiles);
     if (e != cudaSuccess) return e;
-    return launch_pdl(combine_kernel<T, D, NT>, dim3((unsigned)((long long)a.n * c.kv_heads * row_tiles)),
-                      dim3(kCombineThreads), 0, st, c, a, s, row_tiles);
+    return launch_pdl(combine_kernel<T, D, NT>, dim3((unsigned)num_sms, C::kRows / kJoinRows),
+                      dim3(kJoinWarps * kJoinRows * 32), 0, st, c, a, s, row_tiles);
 }
 
 // Row tiles of 8 while a group's rows fit one, else as wide as the registers hold.
@@ -800,9 +993,9 @@ cudaError_t launch_typed(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms,
 }  // namespace
 
 // Two pieces per CTA of the widest row tile.
-size_t kv8_attention_workspace(const Kv8 &c, int n, int, int, int num_sms) {
+size_t kv8_attention_workspace(const Kv8 &c, int num_sms) {
     const int rows = 8 * (c.head_dim == 64 ? wide_tiles<64>() : c.head_dim == 128 ? wide_tiles<128>() : wide_tiles<256>());
-    return 256 + align256((size_t)(n + 1) * 8) + align256((size_t)num_sms * 2 * rows * (c.head_dim + 4) * sizeof(float));
+    return align256((size_t)num_sms * sizeof(int4)) + align256((size_t)num_sms * 2 * rows * (c.head_dim + 4) * sizeof(float));
 }
 
 cudaError_t launch_kv8_attention(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
