@@ -63,8 +63,8 @@ constexpr float kSlack = 8.f;        // how far (base-2 logs) a score may exceed
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
 
-// Shared memory: [ring of every warp | first piece of every warp | scales of every ring place | prefix of the entries'
-// steps | entries | piece table].  A warp leaves at most two pieces, at the start and at the end of its steps; the second
+// Shared memory: [ring of every warp | first piece of every warp | scales of every ring place | where joined rows go |
+// prefix of the entries' steps | entries | piece table].  A warp leaves at most two pieces, at the start and at the end of its steps; the second
 // lies in its ring, which is idle then.
 template <int D, int NT>
 struct Cfg {
@@ -78,7 +78,8 @@ struct Cfg {
     static constexpr int kPiece = kRows * (kPad + 4) * 4;               // outputs, reference, sum, maximum
     static_assert(kPiece <= kRing, "the second piece lies in the ring");
     static constexpr size_t kScaleOff = (size_t)kWarps * (kRing + kPiece);
-    static constexpr size_t kPrefixOff = kScaleOff + kWarps * kStages * 8;
+    static constexpr size_t kJoinOff = kScaleOff + kWarps * kStages * 8;
+    static constexpr size_t kPrefixOff = kJoinOff + 2 * kWarps * kRows * 8;
     static constexpr size_t smem(int n) { return kPrefixOff + (size_t)(n + 1) * 8 + (size_t)n * 16 + kWarps * 2 * 4; }
 };
 
@@ -95,30 +96,35 @@ struct Entry {             // one entry of the call's list
     __device__ __forceinline__ int seen(int query) const { return max(0, min(len, first + query + 1)); }
 };
 
-__device__ __forceinline__ Entry load_entry(const Kv8 &c, const Kv8Query &a, int i, int *bad) {
-    Entry e;
-    e.seq = kv8_seq(a.seqs, i);
-    e.len = e.first = 0;
-    if (e.seq == -1) return e;
-    if ((unsigned)e.seq >= (unsigned)c.max_seqs) {
+// An entry as loaded (len and first only if seq is in the table) made safe: seq -1 and no tokens if it cannot be used.
+__device__ __forceinline__ void check_entry(const Kv8 &c, Entry &e, int *bad) {
+    if (e.seq != -1 && (unsigned)e.seq >= (unsigned)c.max_seqs) {
         *bad |= TP_MLP_KV8_BAD_SEQUENCE;
         e.seq = -1;
-        return e;
-    }
-    e.len = c.lengths[e.seq];
-    if (e.len < 0 || e.len > c.capacity()) {
+    } else if (e.seq >= 0 && (e.len < 0 || e.len > c.capacity())) {
         *bad |= TP_MLP_KV8_BAD_LENGTH;
         e.seq = -1;
-        e.len = 0;
-        return e;
     }
-    e.first = max(-TP_MLP_KV8_MAX_QUERIES, min(e.len, a.positions ? a.positions[i] : e.len - a.q_len));
-    return e;
+    if (e.seq < 0) e.len = 0;
+    e.first = max(-TP_MLP_KV8_MAX_QUERIES, min(e.len, e.first));
 }
 
 // a / b for a >= 0, b > 0, by the short division where it can be.
 __device__ __forceinline__ long long quotient(long long a, int b) {
     return a <= 0x7fffffffLL ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+// The entry that holds step x < prefix[n]: the last with prefix <= x (one warp, 32 probes a round).
+__device__ __forceinline__ int entry_of(const long long *prefix, int n, long long x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const int in = 31 - __clz(__ballot_sync(0xffffffffu, at < hi && prefix[at] <= x));   // (lane 0 always is)
+        hi = min(hi, lo + (in + 1) * step);
+        lo += in * step;
+    }
+    return lo;
 }
 
 // --- register-level pieces ------------------------------------------------------
@@ -290,6 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     int *e_seq = reinterpret_cast<int *>(prefix + n + 1), *e_len = e_seq + n, *e_first = e_len + n;
     int *e_steps = e_first + n;       // of one segment of the entry
     int *piece_seg = e_steps + n;
+    uintptr_t *join_to = reinterpret_cast<uintptr_t *>(smem + C::kJoinOff);
     __shared__ long long scan_part[C::kWarps];
 
     pdl_allow_dependents();
@@ -297,20 +304,32 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
     // 1. the entries, the steps of each, and their prefix sums
     {
-        constexpr int kPer = (kMaxList + C::kThreads - 1) / C::kThreads;
-        long long mine[kPer], sum = 0;
+        constexpr int kMost = (kMaxList + C::kThreads - 1) / C::kThreads;
+        const int per = n <= C::kThreads ? 1 : kMost;   // consecutive entries of a thread
+        long long mine[kMost], sum = 0;
         int bad = 0;
+        Entry en[kMost];
+        // (the loads of all entries before the first use)
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int i = tid * kPer + u;
+        for (int u = 0; u < kMost; ++u) en[u].seq = u < per && tid * per + u < n ? kv8_seq(a.seqs, tid * per + u) : -1;
+#pragma unroll
+        for (int u = 0; u < kMost; ++u) {
+            const bool ok = (unsigned)en[u].seq < (unsigned)c.max_seqs;
+            en[u].len = ok ? c.lengths[en[u].seq] : 0;
+            en[u].first = ok && a.positions ? a.positions[tid * per + u] : en[u].len - a.q_len;
+        }
+#pragma unroll
+        for (int u = 0; u < kMost; ++u) {
+            const int i = tid * per + u;
             mine[u] = sum;
-            if (i < n) {
-                const Entry en = load_entry(c, a, i, &bad);
-                e_seq[i] = en.seq;
-                e_len[i] = en.len;
-                e_first[i] = en.first;
-                e_steps[i] = (en.seen(a.q_len - 1) + kStep - 1) / kStep;
-                sum += (long long)e_steps[i] * units_per_entry;
+            if (u < per && i < n) {
+                check_entry(c, en[u], &bad);
+                const int steps = (en[u].seen(a.q_len - 1) + kStep - 1) / kStep;
+                e_seq[i] = en[u].seq;
+                e_len[i] = en[u].len;
+                e_first[i] = en[u].first;
+                e_steps[i] = steps;
+                sum += (long long)steps * units_per_entry;
             }
         }
         if (bad && blockIdx.x == 0) kv8_flag(c, bad);
@@ -326,9 +345,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) base += w < warp ? scan_part[w] : 0;
 #pragma unroll
-        for (int u = 0; u < kPer; ++u)
-            if (tid * kPer + u <= n) prefix[tid * kPer + u] = base + mine[u];
-        if (n == kPer * C::kThreads && tid == C::kThreads - 1) prefix[n] = base + sum;
+        for (int u = 0; u < kMost; ++u)
+            if (u < per && tid * per + u <= n) prefix[tid * per + u] = base + mine[u];
+        if (n == per * C::kThreads && tid == C::kThreads - 1) prefix[n] = base + sum;
         if (lane < 2) piece_seg[warp * 2 + lane] = -1;
         __syncthreads();
     }
@@ -359,15 +378,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
     // 2. this warp's steps, segment by segment.  The loads run kStages - 1 steps ahead of the products, across segments.
     int e = 0, unit = 0, n_pieces = 0;
-    if (w0 < w1) {   // the entry that holds step w0: the last with prefix <= w0
-        int lo = 0, hi = n;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= w0) lo = mid;
-            else hi = mid;
-        }
-        e = lo;
-    }
+    if (w0 < w1) e = entry_of(prefix, n, w0);
     const int page_steps = c.page_shift - 4;            // log2(steps of a page)
 
     // The loading side: its segment (first step lseg; steps ls .. lend - 1 are this warp's), and the pages of its batch
@@ -795,79 +806,108 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     }
     __syncthreads();
 
-    // 3. join the pieces of each segment, in order; those of a segment that other CTAs share go to the workspace.  A warp
-    // takes a row: lane p first works out piece p's weight in its segment, then the lanes are columns.
+    // 3. join the pieces of each segment, in order; those of a segment that other CTAs share go to the workspace.  First a
+    // thread per (piece, row) works out what the piece's row is multiplied with (and, for the segment's first piece,
+    // where the result goes) ...
     constexpr int kPieces = 2 * C::kWarps;
-    static_assert(kPieces <= 32, "a lane per piece");
-    constexpr int kCols = (D + 127) / 128;                  // float4 columns of a lane
+    static_assert(kPieces < 32, "a lane per piece");
     const int seg = lane < kPieces ? piece_seg[lane] : -1;
-    for (int in_tile = warp; in_tile < C::kRows; in_tile += C::kWarps) {
-        float4 stat = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-        if (seg >= 0) stat = *reinterpret_cast<const float4 *>(piece_at(lane >> 1, lane & 1) + C::kRows * C::kPad + in_tile * 4);
-        float r = stat.x, tp = stat.z, l = 0.f;
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            const bool same = __shfl_sync(0xffffffffu, seg, p) == seg;
-            const float x = __shfl_sync(0xffffffffu, stat.x, p), z = __shfl_sync(0xffffffffu, stat.z, p);
-            r = same ? fmaxf(r, x) : r;
-            tp = same ? fmaxf(tp, z) : tp;
+    const uint32_t live = __ballot_sync(0xffffffffu, seg >= 0);
+    const uint32_t before = live & ((1u << lane) - 1);
+    const int seg_before = __shfl_sync(0xffffffffu, seg, before ? 31 - __clz(before) : lane);
+    const uint32_t starts = __ballot_sync(0xffffffffu, seg >= 0 && (!before || seg_before != seg));
+    // the pieces of the segment whose first piece is p0
+    auto pieces_from = [&](int p0) {
+        const uint32_t later = starts & ~((2u << p0) - 1);
+        return live & ~((1u << p0) - 1) & (later ? (later & -later) - 1 : 0xffffffffu);
+    };
+    for (int x = tid; x < kPieces * C::kRows; x += C::kThreads) {
+        const int p = x / C::kRows, in_tile = x % C::kRows;
+        if (!(live >> p & 1)) continue;
+        auto stat_of = [&](int i) {
+            return reinterpret_cast<float4 *>(piece_at(i >> 1, i & 1) + C::kRows * C::kPad) + in_tile;
+        };
+        const int first = 31 - __clz(starts & ((2u << p) - 1)), sg = piece_seg[p];
+        const uint32_t mine = pieces_from(first);
+        const float own = stat_of(p)->x;
+        float ref = own, l = 0.f, tp = -INFINITY;
+        for (uint32_t m = mine; m; m &= m - 1) ref = fmaxf(ref, stat_of(__ffs(m) - 1)->x);
+        for (uint32_t m = mine; m; m &= m - 1) {
+            const float4 st = *stat_of(__ffs(m) - 1);
+            l += st.y * (st.x == ref ? 1.f : exp2f(st.x - ref));
+            tp = fmaxf(tp, st.z);
         }
-        const float f = seg < 0 ? 0.f : stat.x == r ? 1.f : exp2f(stat.x - r);
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            const bool same = __shfl_sync(0xffffffffu, seg, p) == seg;
-            const float y = __shfl_sync(0xffffffffu, stat.y * f, p);
-            l += same ? y : 0.f;
-        }
-        float4 v[kCols];
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < kPieces; ++p) {
-            const int sg = piece_seg[p];
-            if (sg < 0) continue;
-            const float w = __shfl_sync(0xffffffffu, f, p);
-            const float *pc = piece_at(p >> 1, p & 1) + in_tile * C::kPad + 4 * lane;
-#pragma unroll
-            for (int x = 0; x < kCols; ++x)
-                if (D != 64 || lane < 16) {
-                    const float4 y = *reinterpret_cast<const float4 *>(pc + 128 * x);
-                    v[x].x += y.x * w;
-                    v[x].y += y.y * w;
-                    v[x].z += y.z * w;
-                    v[x].w += y.w * w;
-                }
-            int after = p + 1;   // the segment's last piece?
-            while (after < kPieces && piece_seg[after] < 0) ++after;
-            if (after < kPieces && piece_seg[after] == sg) continue;
-            const float ref_p = __shfl_sync(0xffffffffu, r, p), sum_p = __shfl_sync(0xffffffffu, l, p);
-            const float top_p = __shfl_sync(0xffffffffu, tp, p);
-            const int se = sg / units_per_entry, su = sg - se * units_per_entry, n_steps = e_steps[se];
-            const long long seg0 = prefix[se] + (long long)su * n_steps;
-            if (seg0 >= c0 && seg0 + n_steps <= c1) {
-                const int kv_head = su / row_tiles, tile = su - kv_head * row_tiles, row = tile * C::kRows + in_tile;
+        float f = own == ref ? 1.f : exp2f(own - ref);
+        const int se = sg / units_per_entry, su = sg - se * units_per_entry, n_steps = e_steps[se];
+        const long long seg0 = prefix[se] + (long long)su * n_steps;
+        const int kv_head = su / row_tiles, row = (su - kv_head * row_tiles) * C::kRows + in_tile;
+        uintptr_t to = 0;
+        if (seg0 >= c0 && seg0 + n_steps <= c1) {
+            const RowResult res = row_result(ref, l, tp, a.maximum != nullptr);
+            f *= res.factor;
+            if (row < rows && first == p) {
                 const RowMap map = {se, kv_head, group, a.q_len, a.heads};
-                if (row < rows) write_row<T, D>(a, map.out_row(row), ref_p, sum_p, top_p, v);
-            } else {
-                float *out = ws.pieces + ((size_t)blockIdx.x * 2 + (seg0 < c0 ? 0 : 1)) * (C::kRows * (D + 4));
+                const long long orow = map.out_row(row);
+                to = reinterpret_cast<uintptr_t>(static_cast<T *>(a.o) + orow * D);
+                if (a.maximum) {
+                    a.maximum[orow] = res.maximum;
+                    a.exp_sum[orow] = res.exp_sum;
+                }
+            }
+        } else if (first == p) {
+            float *out = ws.pieces + ((size_t)blockIdx.x * 2 + (seg0 < c0 ? 0 : 1)) * (C::kRows * (D + 4));
+            *reinterpret_cast<float4 *>(out + C::kRows * D + in_tile * 4) = make_float4(ref, l, tp, 0.f);
+            to = reinterpret_cast<uintptr_t>(out + in_tile * D) | 1;   // odd: fp32, not T
+        }
+        reinterpret_cast<float *>(stat_of(p))[3] = f;                   // (the others read only the first three)
+        join_to[x] = first == p ? to : 0;
+    }
+    __syncthreads();
+    // ... then a warp takes two rows of a segment, a lane their columns.
+    constexpr int kCols = (D + 127) / 128, kPairs = C::kRows / 2;
+    const int tasks = __popc(starts) * kPairs;
+    for (int task = warp; task < tasks; task += C::kWarps) {
+        uint32_t left = starts;
+        for (int i = task / kPairs; i > 0; --i) left &= left - 1;
+        const int p0 = __ffs(left) - 1, row0 = task % kPairs * 2;
+        const uint32_t mine = pieces_from(p0);
+        float4 v[2][kCols];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t m = mine; m; m &= m - 1) {
+            const int p = __ffs(m) - 1;
+            const float *pc = piece_at(p >> 1, p & 1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float w = pc[C::kRows * C::kPad + (row0 + k) * 4 + 3];
 #pragma unroll
                 for (int x = 0; x < kCols; ++x)
-                    if (D != 64 || lane < 16) *reinterpret_cast<float4 *>(out + in_tile * D + 4 * (lane + 32 * x)) = v[x];
-                if (lane == 0) *reinterpret_cast<float4 *>(out + C::kRows * D + in_tile * 4) = make_float4(ref_p, sum_p, top_p, 0.f);
+                    if (D != 64 || lane < 16) {
+                        const float4 y = *reinterpret_cast<const float4 *>(pc + (row0 + k) * C::kPad + 4 * (lane + 32 * x));
+                        v[k][x].x += y.x * w;
+                        v[k][x].y += y.y * w;
+                        v[k][x].z += y.z * w;
+                        v[k][x].w += y.w * w;
+                    }
             }
+        }
 #pragma unroll
-            for (int x = 0; x < kCols; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < 2; ++k) {
+            const uintptr_t to = join_to[p0 * C::kRows + row0 + k];
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) {
+                if ((D == 64 && lane >= 16) || to == 0) continue;
+                if (to & 1) reinterpret_cast<float4 *>(to - 1)[lane + 32 * x] = v[k][x];
+                else store4(reinterpret_cast<T *>(to) + 4 * (lane + 32 * x), v[k][x]);
+            }
         }
     }
     // the segment that goes on in the next CTAs, if it began in this one
-    if (tid == 0) {
+    if (warp == C::kWarps - 1) {
         int4 d = make_int4(0, 0, 0, 0);
-        int lo = 0, hi = n;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (prefix[mid] < c1) lo = mid;
-            else hi = mid;
-        }
-        // (the last entry that begins before c1: it holds step c1 - 1)
+        const int lo = entry_of(prefix, n, c1 - 1);
         const int n_steps = e_steps[lo], su = (int)quotient(c1 - 1 - prefix[lo], n_steps);
         const long long seg0 = prefix[lo] + (long long)su * n_steps, seg1 = seg0 + n_steps;
         if (seg0 >= c0 && seg1 > c1) {
@@ -875,7 +915,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             while (first_step(last + 1) < seg1) ++last;
             d = make_int4(lo, su, last - (int)blockIdx.x + 1, 0);
         }
-        ws.shared[blockIdx.x] = d;
+        if (lane == 0) ws.shared[blockIdx.x] = d;
     }
 }
 
