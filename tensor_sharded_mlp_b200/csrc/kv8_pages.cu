@@ -19,7 +19,8 @@
 namespace tpmlp {
 namespace {
 
-constexpr int kMapCtas = 8;
+constexpr int kMapCtas = 8;          // of one cluster, for large pools
+constexpr int kMapOneCta = 16384;    // up to so many pages one CTA ranks them (16 a thread)
 constexpr int kMapThreads = 1024;
 constexpr int kMapWarps = kMapThreads / 32;
 constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
@@ -52,6 +53,11 @@ __device__ __forceinline__ uint32_t cta_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ int cta_count() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return (int)r;
+}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -78,8 +84,9 @@ struct Span {
     int lo, hi;
 };
 __device__ __forceinline__ Span warp_span(const Kv8 &c) {
-    const long long per = (((long long)c.num_pages + kMapCtas * kMapWarps - 1) / (kMapCtas * kMapWarps) + 127) / 128 * 128;
-    const long long lo = per * (cta_rank() * kMapWarps + (threadIdx.x >> 5));
+    const int warps = cta_count() * kMapWarps;
+    const int per = ((c.num_pages + warps - 1) / warps + 127) / 128 * 128;
+    const long long lo = (long long)per * (cta_rank() * kMapWarps + (threadIdx.x >> 5));
     Span s;
     s.lo = (int)min(lo, (long long)c.num_pages);
     s.hi = (int)min(lo + per, (long long)c.num_pages);
@@ -113,10 +120,9 @@ __device__ void rank_free(const Kv8 &c, Span s, int *before, int *all) {
     }
     if (threadIdx.x == 0) cta_n = total;
     cluster_sync();
-    const int rank = (int)cta_rank();
+    const int rank = (int)cta_rank(), ctas = cta_count();
     int sum = 0;
-#pragma unroll
-    for (int r = 0; r < kMapCtas; ++r) {
+    for (int r = 0; r < ctas; ++r) {
         const int v = ld_remote(&cta_n, (uint32_t)r);
         sum += v;
         mine += r < rank ? v : 0;
@@ -149,7 +155,7 @@ __device__ long long block_scan(long long v, long long *sum) {
 
 // Entry i of the list belongs to thread i of every CTA: each CTA works out all
 // entries' needs by itself (the list is short), so only the pool is shared out.
-__global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads)
+__global__ void __launch_bounds__(kMapThreads)
     reserve_kernel(Kv8 c, const int *seqs, const int *counts, int n, PageWs ws) {
     __shared__ int s_seq[kMaxList], s_last[kMaxList], s_len[kMaxList], s_count[kMaxList];
     __shared__ int s_base[kMaxList], s_slot[kMaxList];
@@ -252,7 +258,7 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads)
     cluster_sync();   // the list is complete; every CTA is done with the old map (and with cta_n)
     if (!enough) return;
     const int lane = threadIdx.x & 31;
-    for (int e = (int)cta_rank() * kMapWarps + (threadIdx.x >> 5); e < n; e += kMapCtas * kMapWarps) {
+    for (int e = (int)cta_rank() * kMapWarps + (threadIdx.x >> 5); e < n; e += cta_count() * kMapWarps) {
         const int s = s_seq[e], b = s_base[e], from = s_last[e], l = s_len[e];
         if (s < 0) continue;
         int *row = c.table + (long long)s * c.max_pages;
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // in order, to the free pages in front of L, in order.  A free page p < L is
 // hole number (free pages before p); a used page p >= L is mover number
 // (used pages before p) - (L - H), with H holes.
-__global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads)
+__global__ void __launch_bounds__(kMapThreads)
     compact_map_kernel(Kv8 c, PageWs ws) {
     __shared__ int warp_holes[kMapWarps];
     __shared__ int cta_holes;
@@ -407,10 +413,10 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads)
         cta_holes = h;
     }
     cluster_sync();   // lists complete, refcounts read
+    const int ctas = cta_count();
     int moves = 0;
-#pragma unroll
-    for (int r = 0; r < kMapCtas; ++r) moves += ld_remote(&cta_holes, (uint32_t)r);
-    for (int r = (int)cta_rank() * kMapThreads + threadIdx.x; r < moves; r += kMapCtas * kMapThreads) {
+    for (int r = 0; r < ctas; ++r) moves += ld_remote(&cta_holes, (uint32_t)r);
+    for (int r = (int)cta_rank() * kMapThreads + threadIdx.x; r < moves; r += ctas * kMapThreads) {
         const int from = ws.list[live - moves + r], to = ws.pairs[r].y;
         ws.pairs[r].x = from;
         ws.remap[from] = to;
@@ -504,6 +510,8 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
 }
 
+unsigned map_ctas(const Kv8 &c) { return c.num_pages <= kMapOneCta ? 1 : kMapCtas; }
+
 unsigned copy_grid(const Kv8 &c, long long pairs, int num_sms) {
     const long long tiles = (c.page_bytes() / 16 + kTile - 1) / kTile * c.layers * 2 * pairs;
     const long long most = 8LL * num_sms;   // 8 CTAs of 256 threads fill an SM
@@ -519,7 +527,8 @@ size_t kv8_pages_workspace(const Kv8 &c) {
 cudaError_t launch_kv8_reserve(const Kv8 &c, const int *seqs, const int *counts, int n, void *ws, int num_sms,
                                cudaStream_t st) {
     const PageWs w = page_ws(c, ws);
-    cudaError_t e = launch_pdl(reserve_kernel, dim3(kMapCtas), dim3(kMapThreads), 0, st, c, seqs, counts, n, w);
+    const unsigned ctas = map_ctas(c);
+    cudaError_t e = launch_pdl_cluster(reserve_kernel, dim3(ctas), dim3(kMapThreads), 0, st, ctas, c, seqs, counts, n, w);
     if (e != cudaSuccess) return e;
     return launch_pdl(page_copy_kernel, dim3(copy_grid(c, n, num_sms)), dim3(kCopyThreads), 0, st, c,
                       static_cast<const int2 *>(w.pairs), -1, static_cast<const int *>(w.n_pairs),
@@ -543,7 +552,8 @@ cudaError_t launch_kv8_copy_pages(const Kv8 &c, const int *pairs, int n, int num
 cudaError_t launch_kv8_compact(const Kv8 &c, int *new_index, void *ws, int num_sms, cudaStream_t st) {
     PageWs w = page_ws(c, ws);
     if (new_index) w.remap = new_index;
-    cudaError_t e = launch_pdl(compact_map_kernel, dim3(kMapCtas), dim3(kMapThreads), 0, st, c, w);
+    const unsigned ctas = map_ctas(c);
+    cudaError_t e = launch_pdl_cluster(compact_map_kernel, dim3(ctas), dim3(kMapThreads), 0, st, ctas, c, w);
     if (e != cudaSuccess) return e;
     return launch_pdl(page_copy_kernel, dim3(copy_grid(c, c.num_pages, num_sms)), dim3(kCopyThreads), 0, st, c,
                       static_cast<const int2 *>(w.pairs), -1, static_cast<const int *>(w.n_pairs),
