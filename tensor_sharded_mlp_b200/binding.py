@@ -42,6 +42,7 @@ class Kv8Cache(ctypes.Structure):
     """tp_mlp_kv8_cache: the paged 8-bit key/value cache's buffers and sizes."""
     _fields_ = [(_n, _vp) for _n in ("k", "v", "k_scale", "v_scale", "table", "lengths", "refcount", "status")] + \
                [(_n, _i) for _n in ("layers", "num_pages", "kv_heads", "page_size", "head_dim", "max_seqs", "max_pages")]
+    pages_workspace = None   # bytes, once asked for
 
 
 _kv8 = ctypes.POINTER(Kv8Cache)
@@ -449,6 +450,12 @@ def _rows(t: torch.Tensor, what: str, dims: int, heads: int, head_dim: int) -> i
     return strides[0] if shape[0] > 1 else heads * head_dim
 
 
+def _pages_scratch(cache: Kv8Cache, stream) -> torch.Tensor:
+    if cache.pages_workspace is None:
+        cache.pages_workspace = int(_lib.tp_mlp_kv8_pages_workspace_bytes(cache))
+    return _scratch(cache.pages_workspace, stream)
+
+
 def _kv8_dtype(t: torch.Tensor) -> int:
     return DTYPE["f32" if t.dtype == torch.float32 else "bf16"]
 
@@ -464,7 +471,7 @@ def tp_mlp_kv8_reserve(cache: Kv8Cache, seqs: Optional[torch.Tensor], counts: to
     """Room for counts[i] more tokens in sequence seqs[i] (copy on write of shared last pages)."""
     _list_i32(counts, "counts")
     _list_i32(seqs, "seqs", counts.shape[0])
-    ws = _scratch(int(_lib.tp_mlp_kv8_pages_workspace_bytes(cache)), stream)
+    ws = _pages_scratch(cache, stream)
     _check("tp_mlp_kv8_reserve", _lib.tp_mlp_kv8_reserve(cache, _ptr(seqs), _ptr(counts), counts.shape[0], _ptr(ws),
                                                          ws.numel(), _stream(stream)))
 
@@ -496,7 +503,7 @@ def tp_mlp_kv8_copy_pages(cache: Kv8Cache, pairs: torch.Tensor, stream=None) -> 
 def tp_mlp_kv8_compact(cache: Kv8Cache, new_index: Optional[torch.Tensor] = None, stream=None) -> None:
     """Bring the pages in use to the pool's front; new_index[p] receives page p's new number (-1: it was free)."""
     _list_i32(new_index, "new_index", cache.num_pages)
-    ws = _scratch(int(_lib.tp_mlp_kv8_pages_workspace_bytes(cache)), stream)
+    ws = _pages_scratch(cache, stream)
     _check("tp_mlp_kv8_compact", _lib.tp_mlp_kv8_compact(cache, _ptr(new_index), _ptr(ws), ws.numel(), _stream(stream)))
 
 

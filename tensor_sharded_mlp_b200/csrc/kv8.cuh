@@ -54,7 +54,7 @@ __device__ __forceinline__ float4 e4m3_unpack4(uint32_t w) {
 
 // kv8_append.cu
 cudaError_t launch_kv8_append(const Kv8 &c, const void *k, const void *v, long long row_stride, int tokens,
-                              const int *seqs, const int *cu, int n, int dtype, cudaStream_t st);
+                              const int *seqs, const int *cu, int n, int dtype, int num_sms, cudaStream_t st);
 
 // kv8_attention.cu.  maximum != nullptr: the partial form (o = weighted).
 struct Kv8Query {

@@ -241,8 +241,10 @@ int tp_mlp_kv8_append(const tp_mlp_kv8_cache *cache, int layer, const void *k, c
     if ((s = check_rows(k, tokens, width, row_stride, dtype)) || (s = check_rows(v, tokens, width, row_stride, dtype)))
         return s;
     if ((s = check_list(seqs, n, true)) || (s = check_list(cu_tokens, n + 1, true))) return s;
+    int sms = 0;
+    if ((s = sm_count(&sms))) return s;
     to_layer(&c, layer);
-    return from_cuda(launch_kv8_append(c, k, v, row_stride, tokens, seqs, cu_tokens, n, dtype,
+    return from_cuda(launch_kv8_append(c, k, v, row_stride, tokens, seqs, cu_tokens, n, dtype, sms,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 

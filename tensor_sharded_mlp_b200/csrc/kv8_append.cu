@@ -11,11 +11,11 @@
 //
 // Keys and values of a unit are read once into registers (as far as kKeep
 // vectors a thread hold them; a larger unit is read again, from L2), the two
-// maxima are taken, and the codes are written: HBM-bound for prompts (2 or 4
-// bytes read, 1 written per element).  For a decode step the chain of
-// dependent loads is what counts: the lists go to shared memory in one round
-// trip (where the entry is searched and checked for repeats), then the length,
-// then the table's entry and the rows together.
+// maxima are taken, and the codes are written.  Prompts are HBM-bound (2 or 4
+// bytes read, 1 written per element): a CTA takes a run of units, so that the
+// chain of dependent loads in front of the rows (lists, length, page, refcount)
+// is walked once for all of them.  For a decode step that chain is all there
+// is: a warp takes a unit, and the rows are loaded beside the page's refcount.
 #include <float.h>
 
 #include "common.cuh"
@@ -28,6 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKeep = 4;    // vectors of 8 elements of keys (and of values) a thread keeps between the two passes
 constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
+constexpr int kMaxSlots = 34;
 
 // Eight consecutive elements as loaded.
 template <typename T> struct Vec8;
@@ -61,22 +62,22 @@ __device__ __forceinline__ float finite_max(float m, float x) {
     return a <= FLT_MAX ? fmaxf(m, a) : m;
 }
 
-// Maxima over the group of G threads that works on one unit.
+// Maxima over the group of G threads that works on one unit; `turn` alternates between calls.
 template <int G>
-__device__ __forceinline__ float2 group_max(float2 m) {
+__device__ __forceinline__ float2 group_max(float2 m, int turn) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
         m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
     }
     if (G > 32) {
-        __shared__ float2 part[kThreads / 32];
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+        __shared__ float2 part[2][kThreads / 32];   // (two: a warp may be a call ahead of one that still reads)
+        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = m;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            m.x = fmaxf(m.x, part[w].x);
-            m.y = fmaxf(m.y, part[w].y);
+            m.x = fmaxf(m.x, part[turn][w].x);
+            m.y = fmaxf(m.y, part[turn][w].y);
         }
     }
     return m;
@@ -116,107 +117,110 @@ __device__ __forceinline__ void rescale(uint8_t *codes, int bytes, float ratio, 
     }
 }
 
-// Units: (sequence and page) x kv_heads + head, keys and values together.
-// Without cu, entry i has `slots` page slots; with cu, entry i's slots start at
-// cu[i] / page_size + 2 i: n rows touch at most n / page_size + 2 pages, and
-// floor(a + b) >= floor(a) + floor(b), so the ranges do not overlap.
-// G = 32: a warp per unit; G = kThreads: a CTA per unit.
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads)
-    append_kernel(Kv8 c, const T *k, const T *v, long long row_stride, int tokens, const int *seqs, const int *cu,
-                  int n, int slots, long long units) {
-    __shared__ int s_seq[kMaxList], s_cu[kMaxList + 1];
-    pdl_allow_dependents();
-    const int lane = threadIdx.x & 31, me = threadIdx.x & (G - 1);
-    const long long unit = (long long)blockIdx.x * (kThreads / G) + threadIdx.x / G;
-    pdl_wait_previous();
-    for (int x = threadIdx.x; x <= n; x += kThreads) {
-        if (x < n) s_seq[x] = kv8_seq(seqs, x);
-        if (cu) s_cu[x] = cu[x];
-    }
-    __syncthreads();
-    if (unit >= units) return;
-    const long long slot = unit / c.kv_heads;
-    const int head = (int)(unit - slot * c.kv_heads);
-    const bool teller = head == 0 && me == 0;
+// The rows that a call writes into one page.
+struct Slot {
+    long long row;   // first input row
+    int page;        // -1: nothing to write
+    int a, rows;     // first slot of the page, number
+};
 
+// Lists of the call, in shared memory.
+struct Lists {
+    const int *seq, *cu;   // cu NULL: even shares
+    bool listed;           // the call has a list of sequences (which may repeat itself)
+};
+
+// The slots of a call are pages of its entries.  Without cu, entry i has `each`
+// of them; with cu, entry i's start at cu[i] / page_size + 2 i: n rows touch at
+// most n / page_size + 2 pages, and floor(a + b) >= floor(a) + floor(b), so the
+// ranges do not overlap.  One warp; `teller`: it sets the flags for this slot.
+// The page's refcount is checked by the caller, beside the rows' loads.
+__device__ __forceinline__ Slot find_slot(const Kv8 &c, Lists l, long long slot, int n, int each, int tokens, bool teller) {
+    const int lane = threadIdx.x & 31;
+    Slot out = {0, -1, 0, 0};
+    teller &= lane == 0;
     int i, row0, count;
     long long j;   // which of the entry's pages
-    if (cu) {
+    if (l.cu) {
         // the last entry whose slots start at or before this one: 32 probes a round
         int lo = 0, hi = n;   // start(lo) <= slot < start(hi)
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32;
             const int at = lo + lane * step;
-            const bool in = at < hi && (at == lo || (long long)(s_cu[at] >> c.page_shift) + 2LL * at <= slot);
+            const bool in = at < hi && (at == lo || (long long)(l.cu[at] >> c.page_shift) + 2LL * at <= slot);
             const int k_in = 31 - __clz(__ballot_sync(0xffffffffu, in));   // lane 0 is always in
             hi = min(hi, lo + (k_in + 1) * step);
             lo = lo + k_in * step;
         }
         i = lo;
-        row0 = s_cu[i];
-        const int end = s_cu[i + 1];
+        row0 = l.cu[i];
+        const int end = l.cu[i + 1];
         j = slot - ((long long)(row0 >> c.page_shift) + 2LL * i);
         if (row0 < 0 || end < row0 || end > tokens) {
             if (teller && j == 0) kv8_flag(c, TP_MLP_KV8_BAD_LENGTH);
-            return;
+            return out;
         }
         count = end - row0;
     } else {
-        i = (int)(slot / slots);
-        j = slot - (long long)i * slots;
+        i = (int)(slot / each);
+        j = slot - (long long)i * each;
         count = tokens / n;
         row0 = i * count;
     }
-    if (j < 0 || count == 0) return;
-    const bool first = teller && j == 0;
-    const int seq = s_seq[i];
-    if (seq == -1) return;
-    if ((unsigned)seq >= (unsigned)c.max_seqs || kv8_repeats(seqs ? s_seq : nullptr, i, seq)) {
-        if (first) kv8_flag(c, TP_MLP_KV8_BAD_SEQUENCE);
-        return;
+    const int seq = l.seq[i];
+    if (j < 0 || count == 0 || seq == -1) return out;
+    if ((unsigned)seq >= (unsigned)c.max_seqs || kv8_repeats(l.listed ? l.seq : nullptr, i, seq)) {
+        if (teller && j == 0) kv8_flag(c, TP_MLP_KV8_BAD_SEQUENCE);
+        return out;
     }
     const int len = c.lengths[seq], start = len - count;
     if (start < 0 || len > c.capacity()) {
-        if (first) kv8_flag(c, TP_MLP_KV8_BAD_LENGTH);
-        return;
+        if (teller && j == 0) kv8_flag(c, TP_MLP_KV8_BAD_LENGTH);
+        return out;
     }
     const long long nth = (start >> c.page_shift) + j;
-    if (nth > (len - 1) >> c.page_shift) return;
+    if (nth > (len - 1) >> c.page_shift) return out;
     const int page = c.table[(long long)seq * c.max_pages + nth];
-    const int t0 = j == 0 ? 0 : (int)(nth << c.page_shift) - start;   // first row of this page
-    const int a = j == 0 ? start & (c.page_size - 1) : 0;
-    const int rows = min(c.page_size - a, count - t0);
-    const int D = c.head_dim, per_row = D / 8, vecs = rows * per_row;
+    const int t0 = j == 0 ? 0 : (int)(nth << c.page_shift) - start;   // the page's first row of the entry
+    out.row = row0 + (long long)t0;
+    out.a = j == 0 ? start & (c.page_size - 1) : 0;
+    out.rows = min(c.page_size - out.a, count - t0);
+    if ((unsigned)page < (unsigned)c.num_pages) out.page = page;
+    else if (teller) kv8_flag(c, TP_MLP_KV8_BAD_PAGE);
+    return out;
+}
+
+// One unit, slot (with a page) and head, by a group of G threads.  `checked`: the page is known not to be shared.
+template <typename T, int G>
+__device__ __forceinline__ void append_unit(const Kv8 &c, const T *k, const T *v, long long row_stride, const Slot &sl,
+                                            int head, bool checked, int turn) {
+    const int me = threadIdx.x & (G - 1);
+    const int D = c.head_dim, per_row = D / 8, vecs = sl.rows * per_row, a = sl.a;
     const int row_shift = 31 - __clz(per_row);   // head_dim is a power of two
-    const long long src = (row0 + (long long)t0) * row_stride + (long long)head * D;
+    const long long src = sl.row * row_stride + (long long)head * D;
     auto at = [&](int e) { return src + (long long)(e >> row_shift) * row_stride + (e & (per_row - 1)) * 8; };
     Vec8<T> kk[kKeep], kv[kKeep];
 #pragma unroll
-    for (int u = 0; u < kKeep; ++u) {
-        const int e = me + u * G;
+    for (int x = 0; x < kKeep; ++x) {
+        const int e = me + x * G;
         if (e < vecs) {
-            kk[u].load(k + at(e));
-            kv[u].load(v + at(e));
+            kk[x].load(k + at(e));
+            kv[x].load(v + at(e));
         }
     }
-    if ((unsigned)page >= (unsigned)c.num_pages) {
-        if (teller) kv8_flag(c, TP_MLP_KV8_BAD_PAGE);
+    if (!checked && c.refcount[sl.page] > 1) {
+        if (me == 0 && head == 0) kv8_flag(c, TP_MLP_KV8_SHARED_PAGE);
         return;
     }
-    if (c.refcount[page] > 1) {
-        if (teller) kv8_flag(c, TP_MLP_KV8_SHARED_PAGE);
-        return;
-    }
-    const long long where = (long long)page * c.kv_heads + head;
+    const long long where = (long long)sl.page * c.kv_heads + head;
     // read by all threads before one of them writes it: the maxima's exchange lies between
     const float old_k = a ? c.k_scale[where] : 0.f, old_v = a ? c.v_scale[where] : 0.f;
     float2 amax = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int u = 0; u < kKeep; ++u)
-        if (me + u * G < vecs) {
-            take_max(kk[u], amax.x);
-            take_max(kv[u], amax.y);
+    for (int x = 0; x < kKeep; ++x)
+        if (me + x * G < vecs) {
+            take_max(kk[x], amax.x);
+            take_max(kv[x], amax.y);
         }
     for (int e = me + kKeep * G; e < vecs; e += G) {
         Vec8<T> r, w;
@@ -225,17 +229,17 @@ __global__ void __launch_bounds__(kThreads)
         take_max(r, amax.x);
         take_max(w, amax.y);
     }
-    amax = group_max<G>(amax);
+    amax = group_max<G>(amax, turn);
     const float scale_k = a ? fmaxf(old_k, step_of(amax.x)) : step_of(amax.x);
     const float scale_v = a ? fmaxf(old_v, step_of(amax.y)) : step_of(amax.y);
     const float inv_k = 1.f / scale_k, inv_v = 1.f / scale_v;   // exact for powers of two
     uint8_t *codes_k = c.k + where * c.page_size * D, *codes_v = c.v + where * c.page_size * D;
     const long long skip = (long long)a * D;   // the slots' rows follow each other
 #pragma unroll
-    for (int u = 0; u < kKeep; ++u)
-        if (me + u * G < vecs) {
-            put_codes(codes_k + skip + 8LL * (me + u * G), kk[u], inv_k);
-            put_codes(codes_v + skip + 8LL * (me + u * G), kv[u], inv_v);
+    for (int x = 0; x < kKeep; ++x)
+        if (me + x * G < vecs) {
+            put_codes(codes_k + skip + 8LL * (me + x * G), kk[x], inv_k);
+            put_codes(codes_v + skip + 8LL * (me + x * G), kv[x], inv_v);
         }
     for (int e = me + kKeep * G; e < vecs; e += G) {
         Vec8<T> r, w;
@@ -252,36 +256,96 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+__device__ __forceinline__ Lists take_lists(int *s_seq, int *s_cu, const int *seqs, const int *cu, int n) {
+    for (int x = threadIdx.x; x <= n; x += kThreads) {
+        if (x < n) s_seq[x] = kv8_seq(seqs, x);
+        if (cu) s_cu[x] = cu[x];
+    }
+    __syncthreads();
+    return Lists{s_seq, cu ? s_cu : nullptr, seqs != nullptr};
+}
+
+// A warp per unit (slot x kv_heads + head).
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    append_few_kernel(Kv8 c, const T *k, const T *v, long long row_stride, int tokens, const int *seqs, const int *cu,
+                      int n, int each, long long units) {
+    __shared__ int s_seq[kMaxList], s_cu[kMaxList + 1];
+    pdl_allow_dependents();
+    const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait_previous();
+    const Lists l = take_lists(s_seq, s_cu, seqs, cu, n);
+    if (unit >= units) return;
+    const long long slot = unit / c.kv_heads;
+    const int head = (int)(unit - slot * c.kv_heads);
+    const Slot sl = find_slot(c, l, slot, n, each, tokens, head == 0);
+    if (sl.page >= 0) append_unit<T, 32>(c, k, v, row_stride, sl, head, false, 0);
+}
+
+// The CTA works on the units units * b / grid .. units * (b + 1) / grid - 1 one after the other; its slots (at most
+// kMaxSlots) are found first, a warp each.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
+    append_run_kernel(Kv8 c, const T *k, const T *v, long long row_stride, int tokens, const int *seqs, const int *cu,
+                      int n, int each, long long units) {
+    __shared__ int s_seq[kMaxList], s_cu[kMaxList + 1];
+    __shared__ Slot s_slot[kMaxSlots];
+    pdl_allow_dependents();
+    const long long u0 = units * blockIdx.x / gridDim.x;
+    const int run = (int)(units * (blockIdx.x + 1) / gridDim.x - u0);
+    const long long slot0 = u0 / c.kv_heads;
+    const int head0 = (int)(u0 - slot0 * c.kv_heads);
+    pdl_wait_previous();
+    const Lists l = take_lists(s_seq, s_cu, seqs, cu, n);
+    for (int x = threadIdx.x >> 5; x * c.kv_heads < head0 + run; x += kThreads / 32) {
+        const bool teller = x > 0 || head0 == 0;   // the CTA that holds a slot's first unit sets its flags
+        Slot sl = find_slot(c, l, slot0 + x, n, each, tokens, teller);
+        if (sl.page >= 0 && c.refcount[sl.page] > 1) {
+            if (teller && (threadIdx.x & 31) == 0) kv8_flag(c, TP_MLP_KV8_SHARED_PAGE);
+            sl.page = -1;
+        }
+        if ((threadIdx.x & 31) == 0) s_slot[x] = sl;
+    }
+    __syncthreads();
+    int x = 0, head = head0;
+    for (int u = 0; u < run; ++u) {
+        if (s_slot[x].page >= 0) append_unit<T, kThreads>(c, k, v, row_stride, s_slot[x], head, true, u & 1);
+        if (++head == c.kv_heads) {
+            head = 0;
+            ++x;
+        }
+    }
+}
+
 template <typename T>
 cudaError_t launch_typed(const Kv8 &c, const void *k, const void *v, long long row_stride, int tokens,
-                         const int *seqs, const int *cu, int n, cudaStream_t st) {
-    const int each = (tokens + n - 1) / n;   // rows of an entry; with cu, their mean
-    int slots = 0;
-    long long all;
-    if (cu) {
-        all = (long long)(tokens >> c.page_shift) + 2LL * n;
-    } else {
-        slots = each <= 1 ? 1 : ((each - 2) >> c.page_shift) + 2;
-        all = (long long)slots * n;
-    }
-    const long long units = all * c.kv_heads;
+                         const int *seqs, const int *cu, int n, int num_sms, cudaStream_t st) {
+    const int mean = (tokens + n - 1) / n;   // rows of an entry (with cu: on the mean)
+    const int each = mean <= 1 ? 1 : ((mean - 2) >> c.page_shift) + 2;
+    const long long slots = cu ? (long long)(tokens >> c.page_shift) + 2LL * n : (long long)each * n;
+    const long long units = slots * c.kv_heads;
     const T *tk = static_cast<const T *>(k), *tv = static_cast<const T *>(v);
     // a warp keeps kKeep * 32 vectors: up to there (on the mean) it needs no second read and no barrier
-    if (each * (c.head_dim / 8) <= kKeep * 32) {
+    if (mean * (c.head_dim / 8) <= kKeep * 32) {
         const long long grid = (units + kThreads / 32 - 1) / (kThreads / 32);
-        return launch_pdl(append_kernel<T, 32>, dim3((unsigned)grid), dim3(kThreads), 0, st, c, tk, tv, row_stride,
-                          tokens, seqs, cu, n, slots, units);
+        return launch_pdl(append_few_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, c, tk, tv, row_stride,
+                          tokens, seqs, cu, n, each, units);
     }
-    return launch_pdl(append_kernel<T, kThreads>, dim3((unsigned)units), dim3(kThreads), 0, st, c, tk, tv, row_stride,
-                      tokens, seqs, cu, n, slots, units);
+    // as many CTAs as are resident at once, if their slots fit (a run touches run / kv_heads + 2 slots at most)
+    const long long resident = (long long)num_sms * (sizeof(T) == 2 ? 4 : 2);
+    const long long most = (long long)(kMaxSlots - 2) * c.kv_heads;
+    long long grid = (units + most - 1) / most;
+    if (grid < resident) grid = units < resident ? units : resident;
+    return launch_pdl(append_run_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, c, tk, tv, row_stride, tokens,
+                      seqs, cu, n, each, units);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_append(const Kv8 &c, const void *k, const void *v, long long row_stride, int tokens,
-                              const int *seqs, const int *cu, int n, int dtype, cudaStream_t st) {
-    if (dtype == TP_MLP_F32) return launch_typed<float>(c, k, v, row_stride, tokens, seqs, cu, n, st);
-    return launch_typed<__nv_bfloat16>(c, k, v, row_stride, tokens, seqs, cu, n, st);
+                              const int *seqs, const int *cu, int n, int dtype, int num_sms, cudaStream_t st) {
+    if (dtype == TP_MLP_F32) return launch_typed<float>(c, k, v, row_stride, tokens, seqs, cu, n, num_sms, st);
+    return launch_typed<__nv_bfloat16>(c, k, v, row_stride, tokens, seqs, cu, n, num_sms, st);
 }
 
 }  // namespace tpmlp

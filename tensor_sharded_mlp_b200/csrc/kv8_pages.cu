@@ -7,7 +7,8 @@
 // which makes every result independent of timing.  One cluster of 8 CTAs does
 // that sum: each CTA counts the free pages of an eighth of the pool (16-byte
 // loads, one or two per thread at 64 Ki pages), the CTAs swap their counts
-// through distributed shared memory, and a second walk hands out the ranks.
+// through distributed shared memory, and a second walk hands out the ranks (pools
+// of up to kMapOneCta pages take one CTA, whose threads keep their pages' bits).
 // The data then moves in a second kernel over the whole GPU.
 #include <cuda_runtime.h>
 
@@ -99,15 +100,45 @@ __device__ __forceinline__ uint32_t free_bits(int4 r, int q, int end) {
     return in & ((r.x == 0 ? 1u : 0u) | (r.y == 0 ? 2u : 0u) | (r.z == 0 ? 4u : 0u) | (r.w == 0 ? 8u : 0u));
 }
 
+// The first kAhead * 128 pages' bits of a span, loaded before they are needed: all of it for pools of up to
+// kAhead * 128 * kMapWarps pages a CTA.
+constexpr int kAhead = 4;
+struct Ahead {
+    uint32_t bits;   // 4 of each round
+};
+__device__ __forceinline__ Ahead load_ahead(const Kv8 &c, Span s) {
+    const int lane = threadIdx.x & 31;
+    int4 r[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        const long long q = (long long)s.lo + u * 128 + 4 * lane;
+        r[u] = q < s.hi ? load_refs(c, (int)q) : make_int4(1, 1, 1, 1);
+    }
+    Ahead a = {0};
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        const long long q = (long long)s.lo + u * 128 + 4 * lane;
+        if (q < s.hi) a.bits |= free_bits(r[u], (int)q, s.hi) << (4 * u);
+    }
+    return a;
+}
+// This lane's free bits of the span's round u.
+__device__ __forceinline__ uint32_t round_bits(const Kv8 &c, Span s, Ahead a, int u) {
+    if (u < kAhead) return a.bits >> (4 * u) & 15u;
+    const long long q = (long long)s.lo + u * 128LL + 4 * (threadIdx.x & 31);
+    return q < s.hi ? free_bits(load_refs(c, (int)q), (int)q, s.hi) : 0u;
+}
+__device__ __forceinline__ int rounds_of(Span s) { return (s.hi - s.lo + 127) / 128; }
+
 // Free pages in this warp's span, and the sums over the cluster: *before = free
 // pages in front of the span, *all = free pages of the pool.  Every thread of
 // the cluster calls it; it ends behind a cluster barrier.
-__device__ void rank_free(const Kv8 &c, Span s, int *before, int *all) {
+__device__ void rank_free(const Kv8 &c, Span s, Ahead a, int *before, int *all) {
     __shared__ int warp_n[kMapWarps];
     __shared__ int cta_n;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int n = 0;
-    for (long long q = s.lo + 4 * lane; q < s.hi; q += 128) n += __popc(free_bits(load_refs(c, (int)q), (int)q, s.hi));
+    for (int u = 0; u < rounds_of(s); ++u) n += __popc(round_bits(c, s, a, u));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     if (lane == 0) warp_n[warp] = n;
@@ -129,6 +160,33 @@ __device__ void rank_free(const Kv8 &c, Span s, int *before, int *all) {
     }
     *before = mine;
     *all = sum;
+}
+
+// This lane's place in a round: pages free in front of its first one, given those in front of the round.
+__device__ __forceinline__ int lane_rank(uint32_t bits, int before, int *in_round) {
+    const int lane = threadIdx.x & 31;
+    int x = __popc(bits);
+    const int mine = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    *in_round = __shfl_sync(0xffffffffu, x, 31);
+    return before + x - mine;
+}
+
+// take(page, rank) for the free pages of this warp's span whose rank in the pool is below `total`.
+template <typename Take>
+__device__ __forceinline__ void for_free(const Kv8 &c, Span s, Ahead a, int before, int total, Take take) {
+    for (int u = 0; u < rounds_of(s) && before < total; ++u) {
+        uint32_t bits = round_bits(c, s, a, u);
+        int in_round, rank = lane_rank(bits, before, &in_round);
+        const int q = s.lo + u * 128 + 4 * (threadIdx.x & 31);
+        for (; bits; bits &= bits - 1, ++rank)
+            if (rank < total) take(q + __ffs(bits) - 1, rank);
+        before += in_round;
+    }
 }
 
 // Exclusive prefix sum over the block's threads, and the sum.
@@ -157,20 +215,24 @@ __device__ long long block_scan(long long v, long long *sum) {
 // entries' needs by itself (the list is short), so only the pool is shared out.
 __global__ void __launch_bounds__(kMapThreads)
     reserve_kernel(Kv8 c, const int *seqs, const int *counts, int n, PageWs ws) {
-    __shared__ int s_seq[kMaxList], s_last[kMaxList], s_len[kMaxList], s_count[kMaxList];
-    __shared__ int s_base[kMaxList], s_slot[kMaxList];
-    const int i = threadIdx.x;
-    const bool teller = cta_rank() == 0;   // flags are set once
+    __shared__ int s_seq[kMaxList], s_last[kMaxList], s_len[kMaxList], s_slot[kMaxList];
+    __shared__ long long s_base[kMaxList + 1];
+    const int i = threadIdx.x, lane = threadIdx.x & 31;
+    const bool teller = cta_rank() == 0;   // flags and lengths are written once
     pdl_allow_dependents();
     pdl_wait_previous();
     int seq = -1, count = 0, len = 0, bad = 0;
     if (i < n) {
         seq = kv8_seq(seqs, i);
+        count = counts[i];
         if (seq < -1 || seq >= c.max_seqs) {
             bad |= TP_MLP_KV8_BAD_SEQUENCE;
             seq = -1;
         }
+        if (seq >= 0) len = c.lengths[seq];
     }
+    const Span span = warp_span(c);
+    const Ahead ahead = load_ahead(c, span);   // (on its way while the entries are worked out)
     s_seq[i] = seq;
     __syncthreads();
     if (seq >= 0 && seqs) {
@@ -178,12 +240,9 @@ __global__ void __launch_bounds__(kMapThreads)
         for (int j = 0; j < i; ++j) again |= s_seq[j] == seq;
         if (again) bad |= TP_MLP_KV8_BAD_SEQUENCE;
     }
-    const bool listed = seq >= 0 && !bad;
     int last = -1, refs = 0;
-    bool valid = listed;
-    if (listed) {
-        len = c.lengths[seq];
-        count = counts[i];
+    bool valid = seq >= 0 && !bad;
+    if (valid) {
         if (len < 0 || count < 0 || (long long)len + count > c.capacity()) {
             bad |= TP_MLP_KV8_BAD_LENGTH;
             valid = false;
@@ -213,72 +272,52 @@ __global__ void __launch_bounds__(kMapThreads)
         own_copy = !(here == refs && first);
     }
     if (teller && bad) kv8_flag(c, bad);
-    const int held = c.pages_of(len);
-    const int fresh = valid ? c.pages_of(len + count) - held : 0;
+    const int fresh = valid ? c.pages_of(len + count) - c.pages_of(len) : 0;
     // pages taken in the low 40 bits (at most 2^10 entries of 2^27 pages), copies above
+    constexpr long long kPages = (1LL << 40) - 1;
     long long total;
     const long long scan = block_scan(fresh + (own_copy ? (1LL << 40) + 1 : 0), &total);
-    const long long base = scan & ((1LL << 40) - 1);
-    const int copy_slot = (int)(scan >> 40), copies = (int)(total >> 40);
-    total &= (1LL << 40) - 1;
+    const int copies = (int)(total >> 40);
+    total &= kPages;
+    __syncthreads();   // (s_last is read above)
     s_seq[i] = valid ? seq : -1;
     s_len[i] = len;
-    s_count[i] = count;
-    s_base[i] = (int)base;
+    s_base[i] = scan & kPages;
     s_last[i] = own_copy ? last : -1;
-    s_slot[i] = copy_slot;
-    const Span span = warp_span(c);
+    s_slot[i] = (int)(scan >> 40);
+    if (i == 0) s_base[kMaxList] = total;
+
     int before, all;
-    rank_free(c, span, &before, &all);
+    rank_free(c, span, ahead, &before, &all);
+    // (behind the cluster's barrier: every CTA has read the old map)
     const bool enough = total <= all;
-    if (!enough && teller && threadIdx.x == 0) kv8_flag(c, TP_MLP_KV8_NO_PAGES);
-    if (teller && threadIdx.x == 0) *ws.n_pairs = enough ? copies : 0;
+    if (teller && i == 0) {
+        if (!enough) kv8_flag(c, TP_MLP_KV8_NO_PAGES);
+        *ws.n_pairs = enough ? copies : 0;
+    }
     if (enough) {
-        const int lane = threadIdx.x & 31;
-        for (long long q0 = span.lo; q0 < span.hi && before < total; q0 += 128) {
-            const int q = (int)q0 + 4 * lane;
-            uint32_t bits = q0 + 4 * lane < span.hi ? free_bits(load_refs(c, q), q, span.hi) : 0u;
-            int x = __popc(bits);
-            const int mine = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
+        if (teller && valid) c.lengths[seq] = len + count;
+        // the free page of rank r is the (r - base)-th of the entry whose pages start at base: its copy, then its new ones
+        for_free(c, span, ahead, before, (int)total, [&](int page, int rank) {
+            int lo = 0, hi = kMaxList;   // base(lo) <= rank < base(hi)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_base[mid] <= rank) lo = mid;
+                else hi = mid;
             }
-            int rank = before + x - mine;
-            while (bits) {
-                const int b = __ffs(bits) - 1;
-                bits &= bits - 1;
-                if (rank < total) ws.list[rank] = q + b;
-                ++rank;
-            }
-            before += __shfl_sync(0xffffffffu, x, 31);
-        }
-    }
-    cluster_sync();   // the list is complete; every CTA is done with the old map (and with cta_n)
-    if (!enough) return;
-    const int lane = threadIdx.x & 31;
-    for (int e = (int)cta_rank() * kMapWarps + (threadIdx.x >> 5); e < n; e += cta_count() * kMapWarps) {
-        const int s = s_seq[e], b = s_base[e], from = s_last[e], l = s_len[e];
-        if (s < 0) continue;
-        int *row = c.table + (long long)s * c.max_pages;
-        const int h = c.pages_of(l), end = c.pages_of(l + s_count[e]), skip = from >= 0;
-        for (int k = h + lane; k < end; k += 32) {
-            const int page = ws.list[b + skip + k - h];
-            row[k] = page;
+            const int s = s_seq[lo], l = s_len[lo], from = s_last[lo], nth = rank - (int)s_base[lo];
+            int *row = c.table + (long long)s * c.max_pages;
             c.refcount[page] = 1;
-        }
-        if (lane == 0) {
-            if (from >= 0) {
-                const int page = ws.list[b];
+            if (from >= 0 && nth == 0) {
                 row[l >> c.page_shift] = page;
-                c.refcount[page] = 1;
-                atomicSub(c.refcount + from, 1);
-                ws.pairs[s_slot[e]] = make_int2(from, page);
+                atomicSub(c.refcount + from, 1);   // at least one holder stays: the page is not taken for free
+                ws.pairs[s_slot[lo]] = make_int2(from, page);
+            } else {
+                row[c.pages_of(l) + nth - (from >= 0)] = page;
             }
-            c.lengths[s] = l + s_count[e];
-        }
+        });
     }
+    cluster_sync();   // no CTA leaves while another may still read its count
 }
 
 constexpr int kRowThreads = 128;
@@ -368,21 +407,15 @@ __global__ void __launch_bounds__(kMapThreads)
     pdl_allow_dependents();
     pdl_wait_previous();
     const Span span = warp_span(c);
+    const Ahead ahead = load_ahead(c, span);
     int before, all;
-    rank_free(c, span, &before, &all);
+    rank_free(c, span, ahead, &before, &all);
     const int live = c.num_pages - all;
     int holes = 0;
-    for (long long q0 = span.lo; q0 < span.hi; q0 += 128) {
-        const long long q = q0 + 4 * lane;
-        const uint32_t bits = q < span.hi ? free_bits(load_refs(c, (int)q), (int)q, span.hi) : 0u;
-        int x = __popc(bits);
-        const int mine = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        int rank = before + x - mine;   // free pages before q
+    for (int u = 0; u < rounds_of(span); ++u) {
+        const long long q = (long long)span.lo + u * 128LL + 4 * lane;
+        const uint32_t bits = round_bits(c, span, ahead, u);
+        int in_round, rank = lane_rank(bits, before, &in_round);   // free pages before q
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const long long p = q + b;
@@ -400,7 +433,7 @@ __global__ void __launch_bounds__(kMapThreads)
                 ws.list[p - rank] = (int)p;   // used pages before p
             }
         }
-        before += __shfl_sync(0xffffffffu, x, 31);
+        before += in_round;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) holes += __shfl_xor_sync(0xffffffffu, holes, o);
