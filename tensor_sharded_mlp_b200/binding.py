@@ -114,13 +114,19 @@ def _check(call: str, status: int) -> None:
         raise TpMlpError(call, status)
 
 
+def _current_device() -> int:
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getDevice()
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:   # the current stream's handle, without building a Stream object (0.2 us against 3.5)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(_current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -419,7 +425,7 @@ def _list_i32(t: Optional[torch.Tensor], what: str, n: Optional[int] = None) -> 
 
 
 def _here(t: torch.Tensor) -> bool:
-    return t.is_cuda and t.get_device() == torch.cuda.current_device()
+    return t.is_cuda and t.get_device() == _current_device()
 
 
 def _scratch(nbytes: int, stream) -> torch.Tensor:

@@ -70,7 +70,7 @@ class KvCache8:
         self.c = binding.Kv8Cache(*(ctypes.c_void_p(t.data_ptr()) for t in tensors), *k.shape, *table.shape)
 
     def _on(self):
-        if torch.cuda.current_device() != self.device.index:
+        if binding._current_device() != self.device.index:
             raise ValueError(f"the cache is on {self.device}, which is not the current CUDA device")
         return self.c
 
