@@ -46,6 +46,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv8.cuh"
@@ -56,7 +58,8 @@ namespace tpmlp {
 namespace {
 
 #ifndef KSTAGES
-#define KSTAGES (D == 256 ? 2 : D == 128 ? 4 : 6)
+#define KSTAGES (D == 256 ? 2 : D == 128 ? (NT == 1 ? 5 : 4) : 6)
+#define KPAIR (D * NT <= 128 ? 2 : 1)
 #endif
 constexpr int kStep = 16;            // tokens of one step
 constexpr float kSlack = 8.f;        // how far (base-2 logs) a score may exceed the reference
@@ -72,6 +75,8 @@ struct Cfg {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = 8 * NT;
     static constexpr int kStage = 2 * kStep * D;                       // keys and values of one step
+    // steps whose products are worked on together
+    static constexpr int kPair = KPAIR;
     static constexpr int kStages = KSTAGES;
     static constexpr int kRing = kStage * kStages;
     static constexpr int kPad = D + 4;                                  // floats a piece's row takes
@@ -507,12 +512,185 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         s1 = lend;
         take_batch();
     }
-    int place = 0;
-#pragma unroll 1
-    for (int i = 0; i < C::kStages - 1; ++i) {
-        fetch(i);
-        cp_commit();
-    }
+    // One step's products (kUnits = 1), or two unmasked ones' together: the two chains of dependent instructions
+    // overlap.
+    auto products = [&](auto units, const uint32_t *stage, const float *kscale, const float *vscale) {
+        constexpr int kUnits = decltype(units)::value;
+        // scores: 16 tokens x 8 rows a tile
+        float sc[kUnits][NT][4], sc2[kUnits][NT][4];      // two sums: half as long a chain of dependent products
+#pragma unroll
+        for (int y = 0; y < kUnits; ++y)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[y][nt][k] = sc2[y][nt][k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int y = 0; y < kUnits; ++y) {
+                const uint4 lo4 = lds128(stage[y] + chunk_at<D>(g, key_chunk<D>(t, i)));
+                const uint4 hi4 = lds128(stage[y] + chunk_at<D>(g + 8, key_chunk<D>(t, i)));
+                const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3_to_f16(lo[w], a0, a2);
+                    e4m3_to_f16(hi[w], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int pt = 0; pt < kParts; ++pt)
+                            mma(w & 1 ? sc2[y][nt] : sc[y][nt], a0, a1, a2, a3, q[pt][nt][4 * i + w][0],
+                                q[pt][nt][4 * i + w][1]);
+                }
+            }
+        // base-2 scores; vlog: the binade above the value scale
+        float vlog[kUnits];
+        const bool masked = kUnits == 1 && s >= plain;
+        bool rise = false;
+#pragma unroll
+        for (int y = 0; y < kUnits; ++y) {
+            vlog[y] = (float)max((int)(__float_as_uint(vscale[y]) >> 23) - 126, -100);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float x = (sc[y][nt][k] + sc2[y][nt][k]) * (fac[nt][k & 1] * kscale[y]);
+                    if (masked && s * kStep + g + 8 * (k >> 1) >= limit[nt][k & 1]) x = -INFINITY;
+                    sc[y][nt][k] = x;
+                    rise |= x + vlog[y] > ref[nt][k & 1] + kSlack;
+                    top[nt][k & 1] = fmaxf(top[nt][k & 1], x);
+                }
+        }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int y = 0; y < kUnits; ++y) m = fmaxf(m, fmaxf(sc[y][nt][x], sc[y][nt][x + 2]) + vlog[y]);
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    m = fmaxf(ref[nt][x], m);
+                    const float turn = m == ref[nt][x] ? 1.f : exp2_fast(ref[nt][x] - m);
+                    ref[nt][x] = m;
+                    sum[nt][x] *= turn;
+#pragma unroll
+                    for (int mt = 0; mt < kMt; ++mt) {
+                        o[nt][mt][x] *= turn;
+                        o[nt][mt][x + 2] *= turn;
+                    }
+                }
+        }
+        uint32_t w[kUnits][kParts][NT][2];      // weights as the second product's B operand
+#pragma unroll
+        for (int y = 0; y < kUnits; ++y)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    p[k] = exp2_fast(sc[y][nt][k] - ref[nt][k & 1]);
+                    sum[nt][k & 1] += p[k];
+                    p[k] *= vscale[y];
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t h = f16x2(p[2 * x], p[2 * x + 1]);
+                    w[y][0][nt][x] = transpose8x8(h);
+                    if (kExact) {
+                        const float2 b = widen_f16x2(h);
+                        w[y][kParts - 1][nt][x] = transpose8x8(f16x2(p[2 * x] - b.x, p[2 * x + 1] - b.y));
+                    }
+                }
+            }
+
+        // outputs: tokens 2t, 2t+1, 2t+8, 2t+9 of this thread, D / 8 columns from g on
+#pragma unroll
+        for (int y = 0; y < kUnits; ++y) {
+            const uint32_t vals = stage[y] + kStep * D;
+            uint32_t v[4][D / 32];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 2 * t + (k & 1) + 8 * (k >> 1);
+                if (D == 64) {
+                    const uint2 x = lds64(vals + r * D + g * 8);
+                    v[k][0] = x.x;
+                    v[k][1] = x.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i) {
+                        const uint4 x = lds128(vals + chunk_at<D>(r, g + 8 * i));
+                        v[k][4 * i] = x.x;
+                        v[k][4 * i + 1] = x.y;
+                        v[k][4 * i + 2] = x.z;
+                        v[k][4 * i + 3] = x.w;
+                    }
+                }
+            }
+            if (masked) {   // a NaN value must not reach rows that do not see its token (0 * NaN)
+                uint32_t any = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) any |= nan_bytes(v[k][i]);
+                if (__any_sync(0xffffffffu, any != 0)) {
+                    uint32_t see[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int tok = s * kStep + g + 8 * x;
+                            see[nt][x] = transpose8x8(f16x2(tok < limit[nt][0] ? 1.f : 0.f, tok < limit[nt][1] ? 1.f : 0.f));
+                        }
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t nb[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            nb[k] = nan_bytes(v[k][i]);
+                            v[k][i] &= ~nb[k];
+                            nb[k] &= 0x38383838u;           // e4m3's 1
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t sel = h ? 0x7362u : 0x5140u;
+                            uint32_t a0, a1, a2, a3;
+                            e4m3_to_f16(__byte_perm(nb[0], nb[1], sel), a0, a1);
+                            e4m3_to_f16(__byte_perm(nb[2], nb[3], sel), a2, a3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma(hit, a0, a1, a2, a3, see[nt][0], see[nt][1]);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (hit[k] > 0.f) o[nt][2 * i + h][k] = NAN;
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t sel = h ? 0x7362u : 0x5140u;   // (token, token + 1) pairs of two columns
+                    uint32_t a0, a1, a2, a3;
+                    e4m3_to_f16(__byte_perm(v[0][i], v[1][i], sel), a0, a1);
+                    e4m3_to_f16(__byte_perm(v[2][i], v[3][i], sel), a2, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int pt = 0; pt < kParts; ++pt)
+                            mma(o[nt][2 * i + h], a0, a1, a2, a3, w[y][pt][nt][0], w[y][pt][nt][1]);
+                }
+        }
+    };
+    // The ring: the products read at `place`, the next fetch goes to next_place; n_free places were read since the last
+    // fetch.  Fetches fill the whole ring, so kStages - kPair groups may be open when the oldest kPair are needed.
+    int place = 0, next_place = 0, n_free = C::kStages;
     for (long long at = w0; at < w1;) {
         {
             const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
@@ -569,172 +747,37 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 sum[nt][0] = sum[nt][1] = 0.f;
             }
         }
-        for (; s < s1; ++s) {
-            cp_wait<C::kStages - 2>();
+        while (s < s1) {
+            __syncwarp();   // every lane is done with the places that these fetches refill
+            for (; n_free > 0; --n_free) {
+                fetch(next_place);
+                cp_commit();
+                next_place = next_place + 1 == C::kStages ? 0 : next_place + 1;
+            }
+            cp_wait<C::kStages - C::kPair>();
             __syncwarp();
-            // (every lane is done with the place that this fetch refills: it was read a step ago)
-            fetch(place == 0 ? C::kStages - 1 : place - 1);
-            cp_commit();
-            const uint32_t keys = ring + place * C::kStage, vals = keys + kStep * D;
-            const uint2 pair = lds64(scales + place * 8);
-            const float kscale = __uint_as_float(pair.x), vscale = __uint_as_float(pair.y);
-            place = place + 1 == C::kStages ? 0 : place + 1;
-            if (vscale < 0.f) continue;                     // not a page of the pool: nothing is seen
-            // scores: 16 tokens x 8 rows a tile
-            float sc[NT][4], sc2[NT][4];      // two sums: half as long a chain of dependent products
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sc[nt][k] = sc2[nt][k] = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const uint4 lo4 = lds128(keys + chunk_at<D>(g, key_chunk<D>(t, i)));
-                const uint4 hi4 = lds128(keys + chunk_at<D>(g + 8, key_chunk<D>(t, i)));
-                const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t a0, a1, a2, a3;
-                    e4m3_to_f16(lo[w], a0, a2);
-                    e4m3_to_f16(hi[w], a1, a3);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int pt = 0; pt < kParts; ++pt)
-                            mma(w & 1 ? sc2[nt] : sc[nt], a0, a1, a2, a3, q[pt][nt][4 * i + w][0], q[pt][nt][4 * i + w][1]);
+            const int place1 = place + 1 == C::kStages ? 0 : place + 1;
+            const uint2 pair0 = lds64(scales + place * 8);
+            if (C::kPair == 2 && s + 2 <= s1 && s + 2 <= plain) {
+                const uint2 pair1 = lds64(scales + place1 * 8);
+                const uint32_t at2[2] = {ring + place * C::kStage, ring + place1 * C::kStage};
+                const float ks[2] = {__uint_as_float(pair0.x), __uint_as_float(pair1.x)};
+                const float vs[2] = {__uint_as_float(pair0.y), __uint_as_float(pair1.y)};
+                if (fminf(vs[0], vs[1]) >= 0.f) {
+                    products(std::integral_constant<int, C::kPair>{}, at2, ks, vs);
+                    s += 2;
+                    n_free = 2;
+                    place = place1 + 1 == C::kStages ? 0 : place1 + 1;
+                    continue;
                 }
             }
-            // base-2 scores; the binade above the value scale
-            const int vexp = max((int)(__float_as_uint(vscale) >> 23) - 126, -100);
-            const float vlog = (float)vexp;
-            const bool masked = s >= plain;
-            bool rise = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float x = (sc[nt][k] + sc2[nt][k]) * (fac[nt][k & 1] * kscale);
-                    if (masked && s * kStep + g + 8 * (k >> 1) >= limit[nt][k & 1]) x = -INFINITY;
-                    sc[nt][k] = x;
-                    rise |= x + vlog > ref[nt][k & 1] + kSlack;
-                    top[nt][k & 1] = fmaxf(top[nt][k & 1], x);
-                }
-            if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float m = fmaxf(sc[nt][x], sc[nt][x + 2]);
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m = fmaxf(ref[nt][x], m + vlog);
-                        const float turn = m == ref[nt][x] ? 1.f : exp2_fast(ref[nt][x] - m);
-                        ref[nt][x] = m;
-                        sum[nt][x] *= turn;
-#pragma unroll
-                        for (int mt = 0; mt < kMt; ++mt) {
-                            o[nt][mt][x] *= turn;
-                            o[nt][mt][x + 2] *= turn;
-                        }
-                    }
-            }
-            uint32_t w[kParts][NT][2];      // weights as the second product's B operand
-            uint32_t see[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    p[k] = exp2_fast(sc[nt][k] - ref[nt][k & 1]);
-                    sum[nt][k & 1] += p[k];
-                    p[k] *= vscale;
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t h = f16x2(p[2 * x], p[2 * x + 1]);
-                    w[0][nt][x] = transpose8x8(h);
-                    if (kExact) {
-                        const float2 b = widen_f16x2(h);
-                        w[kParts - 1][nt][x] = transpose8x8(f16x2(p[2 * x] - b.x, p[2 * x + 1] - b.y));
-                    }
-                }
-            }
-
-            // outputs: tokens 2t, 2t+1, 2t+8, 2t+9 of this thread, D / 8 columns from g on
-            uint32_t v[4][D / 32];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 2 * t + (k & 1) + 8 * (k >> 1);
-                if (D == 64) {
-                    const uint2 x = lds64(vals + r * D + g * 8);
-                    v[k][0] = x.x;
-                    v[k][1] = x.y;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 128; ++i) {
-                        const uint4 x = lds128(vals + chunk_at<D>(r, g + 8 * i));
-                        v[k][4 * i] = x.x;
-                        v[k][4 * i + 1] = x.y;
-                        v[k][4 * i + 2] = x.z;
-                        v[k][4 * i + 3] = x.w;
-                    }
-                }
-            }
-            if (masked) {   // a NaN value must not reach rows that do not see its token (0 * NaN)
-                uint32_t any = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) any |= nan_bytes(v[k][i]);
-                if (__any_sync(0xffffffffu, any != 0)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int tok = s * kStep + g + 8 * x;
-                            see[nt][x] = transpose8x8(f16x2(tok < limit[nt][0] ? 1.f : 0.f, tok < limit[nt][1] ? 1.f : 0.f));
-                        }
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t nb[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            nb[k] = nan_bytes(v[k][i]);
-                            v[k][i] &= ~nb[k];
-                            nb[k] &= 0x38383838u;           // e4m3's 1
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t sel = h ? 0x7362u : 0x5140u;
-                            uint32_t a0, a1, a2, a3;
-                            e4m3_to_f16(__byte_perm(nb[0], nb[1], sel), a0, a1);
-                            e4m3_to_f16(__byte_perm(nb[2], nb[3], sel), a2, a3);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma(hit, a0, a1, a2, a3, see[nt][0], see[nt][1]);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (hit[k] > 0.f) o[nt][2 * i + h][k] = NAN;
-                            }
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t sel = h ? 0x7362u : 0x5140u;   // (token, token + 1) pairs of two columns
-                    uint32_t a0, a1, a2, a3;
-                    e4m3_to_f16(__byte_perm(v[0][i], v[1][i], sel), a0, a1);
-                    e4m3_to_f16(__byte_perm(v[2][i], v[3][i], sel), a2, a3);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int pt = 0; pt < kParts; ++pt)
-                            mma(o[nt][2 * i + h], a0, a1, a2, a3, w[pt][nt][0], w[pt][nt][1]);
-                }
+            const uint32_t at1[1] = {ring + place * C::kStage};
+            const float ks[1] = {__uint_as_float(pair0.x)}, vs[1] = {__uint_as_float(pair0.y)};
+            // (a negative value scale: not a page of the pool, nothing is seen)
+            if (!(vs[0] < 0.f)) products(std::integral_constant<int, 1>{}, at1, ks, vs);
+            ++s;
+            n_free = 1;
+            place = place1;
         }
         at += s1 - s0;
 
