@@ -906,24 +906,24 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         join_to[x] = first == p ? to : 0;
     }
     __syncthreads();
-    // ... then a warp takes two rows of a segment, a lane their columns.
-    constexpr int kCols = (D + 127) / 128, kPairs = C::kRows / 2;
-    const int tasks = __popc(starts) * kPairs;
+    // ... then a warp takes kRowsPer rows of a segment, a lane their columns.
+    constexpr int kCols = (D + 127) / 128, kRowsPer = 4, kGroups = C::kRows / kRowsPer;
+    const int tasks = __popc(starts) * kGroups;
     for (int task = warp; task < tasks; task += C::kWarps) {
         uint32_t left = starts;
-        for (int i = task / kPairs; i > 0; --i) left &= left - 1;
-        const int p0 = __ffs(left) - 1, row0 = task % kPairs * 2;
+        for (int i = task / kGroups; i > 0; --i) left &= left - 1;
+        const int p0 = __ffs(left) - 1, row0 = task % kGroups * kRowsPer;
         const uint32_t mine = pieces_from(p0);
-        float4 v[2][kCols];
+        float4 v[kRowsPer][kCols];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < kRowsPer; ++k)
 #pragma unroll
             for (int x = 0; x < kCols; ++x) v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (uint32_t m = mine; m; m &= m - 1) {
             const int p = __ffs(m) - 1;
             const float *pc = piece_at(p >> 1, p & 1);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < kRowsPer; ++k) {
                 const float w = pc[C::kRows * C::kPad + (row0 + k) * 4 + 3];
 #pragma unroll
                 for (int x = 0; x < kCols; ++x)
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kRowsPer; ++k) {
             const uintptr_t to = join_to[p0 * C::kRows + row0 + k];
 #pragma unroll
             for (int x = 0; x < kCols; ++x) {
