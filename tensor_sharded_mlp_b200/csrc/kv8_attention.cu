@@ -57,11 +57,8 @@
 namespace tpmlp {
 namespace {
 
-#ifndef KSTAGES
-#define KSTAGES (D == 256 ? 2 : D == 128 ? (NT == 1 ? 5 : 4) : 6)
-#define KPAIR (D * NT <= 128 ? 2 : 1)
-#endif
 constexpr int kStep = 16;            // tokens of one step
+constexpr int kOpen = 3;             // steps that a segment's start and end cost beside its own, about
 constexpr float kSlack = 8.f;        // how far (base-2 logs) a score may exceed the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
@@ -76,8 +73,8 @@ struct Cfg {
     static constexpr int kRows = 8 * NT;
     static constexpr int kStage = 2 * kStep * D;                       // keys and values of one step
     // steps whose products are worked on together
-    static constexpr int kPair = KPAIR;
-    static constexpr int kStages = KSTAGES;
+    static constexpr int kPair = D * NT <= 128 ? 2 : 1;
+    static constexpr int kStages = D == 256 ? 2 : D == 64 ? 6 : NT == 1 ? 5 : 4;
     static constexpr int kRing = kStage * kStages;
     static constexpr int kPad = D + 4;                                  // floats a piece's row takes
     static constexpr int kPiece = kRows * (kPad + 4) * 4;               // outputs, reference, sum, maximum
@@ -307,7 +304,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     pdl_allow_dependents();
     pdl_wait_previous();
 
-    // 1. the entries, the steps of each, and their prefix sums
+    // 1. the entries, the steps of each, and their prefix sums.  A segment takes kOpen places in front of its steps, so
+    // that many short ones are not a warp's lot.
     {
         constexpr int kMost = (kMaxList + C::kThreads - 1) / C::kThreads;
         const int per = n <= C::kThreads ? 1 : kMost;   // consecutive entries of a thread
@@ -334,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 e_len[i] = en[u].len;
                 e_first[i] = en[u].first;
                 e_steps[i] = steps;
-                sum += (long long)steps * units_per_entry;
+                sum += (long long)(steps ? steps + kOpen : 0) * units_per_entry;
             }
         }
         if (bad && blockIdx.x == 0) kv8_flag(c, bad);
@@ -386,7 +384,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     if (w0 < w1) e = entry_of(prefix, n, w0);
     const int page_steps = c.page_shift - 4;            // log2(steps of a page)
 
-    // The loading side: its segment (first step lseg; steps ls .. lend - 1 are this warp's), and the pages of its batch
+    // The loading side: its segment (first step at lseg; steps ls .. lend - 1 are this warp's), and the pages of its batch
     // of 32 (lane x holds the x-th); the next batch's page numbers (of this segment, or the next one's first) are loaded
     // while this one is in use.  key_ptr and scale_ptr move on from step to step within a page.
     int le = e, lunit = 0, ls = 0, lend = 0, lbatch = 0, lpage = 0, npage = 0, llen = 0, lhead = 0;
@@ -407,7 +405,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         lpage = ok ? npage : -1;
         if ((lend - 1) >> (page_steps + 5) > lbatch) {
             npage = load_pages(le, lbatch + 1);
-        } else if (lseg + lend < w1) {
+        } else if (lseg + lend + kOpen < w1) {
             int i = le;
             if (lunit + 1 == units_per_entry)
                 do ++i;
@@ -415,25 +413,26 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             npage = load_pages(i, 0);
         }
     };
-    if (w0 < w1) {
+    bool work = w0 < w1;
+    if (work) {
         const int steps = e_steps[e];
-        unit = lunit = (int)quotient(w0 - prefix[e], steps);
+        unit = lunit = (int)quotient(w0 - prefix[e], steps + kOpen);
         lhead = lunit / row_tiles;
         llen = e_len[e];
-        lseg = prefix[e] + (long long)lunit * steps;
-        ls = (int)(w0 - lseg);
-        lend = (int)min((long long)steps, w1 - lseg);
+        lseg = prefix[e] + (long long)lunit * (steps + kOpen) + kOpen;
+        work = lseg < w1;
+    }
+    if (work) {
+        ls = (int)max(0LL, w0 - lseg);
+        lend = (int)min((long long)e_steps[e], w1 - lseg);
         lbatch = ls >> (page_steps + 5);
         npage = load_pages(e, lbatch);
     }
     bool turn_page = true;
     auto fetch = [&](int place) {
         if (ls == lend) {                                  // the next segment
-            lseg += lend;
-            if (lseg >= w1) {
-                lend = ls = 0;
-                return;
-            }
+            if (lseg + lend + kOpen >= w1) return;
+            lseg += lend + kOpen;
             if (++lunit == units_per_entry) {
                 lunit = 0;
                 do ++le;
@@ -483,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (key_ptr) key_ptr += kStep * D;
     };
     // The products' side: segment (e, unit), of which this warp has steps s0 .. s1 - 1 and is at s.
-    constexpr bool kAhead = NT == 1 && !kExact;   // queries are loaded ahead where the registers hold them
+    constexpr bool kAhead = NT == 1 && (!kExact || D == 64);   // queries are loaded ahead where the registers hold them
     RawQuery<T> raw[NT][D / 32];
     auto load_queries = [&]() {
         const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
@@ -505,7 +504,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     int plain = 0;
     float o[NT][kMt][4], ref[NT][2], sum[NT][2], top[NT][2];
     int steps = 0, s0 = 0, s1 = 0, s = 0;
-    if (w0 < w1) {
+    long long first = lseg;   // where the segment's steps begin
+    if (work) {
         if (kAhead) load_queries();
         steps = e_steps[e];
         s = s0 = ls;
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     // The ring: the products read at `place`, the next fetch goes to next_place; n_free places were read since the last
     // fetch.  Fetches fill the whole ring, so kStages - kPair groups may be open when the oldest kPair are needed.
     int place = 0, next_place = 0, n_free = C::kStages;
-    for (long long at = w0; at < w1;) {
+    while (work) {
         {
             const int kv_head = unit / row_tiles, tile = unit - kv_head * row_tiles;
             if (!kAhead) load_queries();
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                         }
                     }
                 }
-                const float up = have ? ldexpf(a.scale * kLog2e, ex) : 0.f;
+                const float up = have ? a.scale * kLog2e * __uint_as_float((uint32_t)(ex + 127) << 23) : 0.f;
                 const int lim = have ? en.seen(map.query(r)) : 0x7fffffff;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -779,12 +779,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             n_free = 1;
             place = place1;
         }
-        at += s1 - s0;
 
         // the segment's end: its rows, or a piece of them
         const int done_e = e, done_unit = unit;
         const bool whole = s0 == 0 && s1 == steps;
-        if (at < w1) {
+        first += s1 + kOpen;
+        work = first < w1;
+        if (work) {
             if (++unit == units_per_entry) {
                 unit = 0;
                 do ++e;
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 steps = e_steps[e];
             }
             s = s0 = 0;
-            s1 = (int)min((long long)steps, w1 - at);
+            s1 = (int)min((long long)steps, w1 - first);
             if (kAhead) load_queries();
         }
 #pragma unroll
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         float f = own == ref ? 1.f : exp2f(own - ref);
         const int se = sg / units_per_entry, su = sg - se * units_per_entry, n_steps = e_steps[se];
-        const long long seg0 = prefix[se] + (long long)su * n_steps;
+        const long long seg0 = prefix[se] + (long long)su * (n_steps + kOpen) + kOpen;
         const int kv_head = su / row_tiles, row = (su - kv_head * row_tiles) * C::kRows + in_tile;
         uintptr_t to = 0;
         if (seg0 >= c0 && seg0 + n_steps <= c1) {
@@ -951,9 +952,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     if (warp == C::kWarps - 1) {
         int4 d = make_int4(0, 0, 0, 0);
         const int lo = entry_of(prefix, n, c1 - 1);
-        const int n_steps = e_steps[lo], su = (int)quotient(c1 - 1 - prefix[lo], n_steps);
-        const long long seg0 = prefix[lo] + (long long)su * n_steps, seg1 = seg0 + n_steps;
-        if (seg0 >= c0 && seg1 > c1) {
+        const int n_steps = e_steps[lo], su = (int)quotient(c1 - 1 - prefix[lo], n_steps + kOpen);
+        const long long seg0 = prefix[lo] + (long long)su * (n_steps + kOpen) + kOpen, seg1 = seg0 + n_steps;
+        if (seg0 >= c0 && seg0 < c1 && seg1 > c1) {
             int last = blockIdx.x + 1;
             while (first_step(last + 1) < seg1) ++last;
             d = make_int4(lo, su, last - (int)blockIdx.x + 1, 0);
