@@ -538,6 +538,11 @@ int tp_mlp_copy_async(void *dst, const void *src, size_t bytes, tp_mlp_stream_t 
  * left out, nothing outside the buffers is touched, and a bit of *status is
  * set (tp_mlp_kv8_get_status).  A sequence number of -1 marks an unused entry
  * of a list (a padded batch) and is passed over without a flag.
+ *
+ * Order: calls that change the map or the pages must not overlap other calls
+ * on the same cache (one stream, or events); attention calls may overlap each
+ * other.  Every call may be captured in a CUDA graph.  Inputs, outputs and
+ * workspaces must not overlap the cache's buffers or each other.
  */
 typedef struct {
     void *k, *v;               /* e4m3, layers x num_pages x kv_heads x page_size x head_dim */

@@ -60,12 +60,13 @@ namespace {
 constexpr int kStep = 16;            // tokens of one step
 constexpr int kOpen = 3;             // steps that a segment's start and end cost beside its own, about
 constexpr float kSlack = 8.f;        // how far (base-2 logs) a score may exceed the reference
+constexpr int kLeastLog = -88;       // smallest binade of a value scale in R: 2^31 weights of 2^(8 + 88) have a finite sum
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
 
 // Shared memory: [ring of every warp | first piece of every warp | scales of every ring place | where joined rows go |
-// prefix of the entries' steps | entries | piece table].  A warp leaves at most two pieces, at the start and at the end of its steps; the second
-// lies in its ring, which is idle then.
+// prefix of the entries' steps | entries | piece table].  A warp leaves at most two pieces, at the start and at the end
+// of its steps; the second lies in its ring, which is idle then.
 template <int D, int NT>
 struct Cfg {
     static constexpr int kWarps = 8;
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         bool rise = false;
 #pragma unroll
         for (int y = 0; y < kUnits; ++y) {
-            vlog[y] = (float)max((int)(__float_as_uint(vscale[y]) >> 23) - 126, -100);
+            vlog[y] = (float)max((int)(__float_as_uint(vscale[y]) >> 23) - 126, kLeastLog);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -964,14 +965,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 }
 
 // Joins the pieces of the segments that several CTAs share.  kJoinWarps warps take a row: warp w the pieces w, w +
-// kJoinWarps, ...; their sums meet in shared memory.
-constexpr int kJoinWarps = 4, kJoinRows = 2;
+// kJoinWarps, ...; their sums meet in shared memory.  A CTA has kJoinThreads / 32 / kJoinWarps rows.
+constexpr int kJoinThreads = 256;
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kJoinWarps * kJoinRows * 32)
+template <typename T, int D, int NT, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinThreads)
     combine_kernel(Kv8 c, Kv8Query a, Split ws, int row_tiles) {
     using C = Cfg<D, NT>;
-    constexpr int kCols = (D + 127) / 128;
+    constexpr int kCols = (D + 127) / 128, kJoinRows = kJoinThreads / 32 / kJoinWarps;
     __shared__ float4 part[kJoinRows][kJoinWarps][kCols * 32];
     __shared__ float4 part_stat[kJoinRows][kJoinWarps];
     pdl_allow_dependents();
@@ -1045,6 +1046,7 @@ Split split_of(void *ws, int num_sms) {
 template <typename T, int D, int NT>
 cudaError_t launch_tile(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
     using C = Cfg<D, NT>;
+    static_assert(C::smem(kMaxList) <= 227 * 1024 - 256, "shared memory of an SM");
     const int rows = a.q_len * (a.heads / c.kv_heads), row_tiles = (rows + C::kRows - 1) / C::kRows;
     const Split s = split_of(ws, num_sms);
     auto kern = attention_kernel<T, D, NT>;
@@ -1052,8 +1054,15 @@ cudaError_t launch_tile(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, 
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)num_sms), dim3(C::kThreads), C::smem(a.n), st, c, a, s, row_tiles);
     if (e != cudaSuccess) return e;
-    return launch_pdl(combine_kernel<T, D, NT>, dim3((unsigned)num_sms, C::kRows / kJoinRows),
-                      dim3(kJoinWarps * kJoinRows * 32), 0, st, c, a, s, row_tiles);
+    // Eight warps a row where a segment has many pieces, four (half as many CTAs) otherwise: one sequence of 200000
+    // tokens with one KV head 26.3 against 30.8 us, of 20000 with two 14.5 / 17.2, of 4099 with eight 12.0 / 12.3;
+    // 16 sequences of 4000 with eight (128 segments) 32.7 / 31.9, 32 ragged ones 44.8 / 44.0.
+    const long long segments = (long long)a.n * c.kv_heads * row_tiles;
+    if (segments * 8 <= num_sms)
+        return launch_pdl(combine_kernel<T, D, NT, 8>, dim3((unsigned)num_sms, C::kRows), dim3(kJoinThreads), 0, st, c, a,
+                          s, row_tiles);
+    return launch_pdl(combine_kernel<T, D, NT, 4>, dim3((unsigned)num_sms, C::kRows / 2), dim3(kJoinThreads), 0, st, c, a,
+                      s, row_tiles);
 }
 
 // Row tiles of 8 while a group's rows fit one, else as wide as the registers hold.

@@ -216,7 +216,7 @@ __device__ long long block_scan(long long v, long long *sum) {
 __global__ void __launch_bounds__(kMapThreads)
     reserve_kernel(Kv8 c, const int *seqs, const int *counts, int n, PageWs ws) {
     __shared__ int s_seq[kMaxList], s_last[kMaxList], s_len[kMaxList], s_slot[kMaxList];
-    __shared__ long long s_base[kMaxList + 1];
+    __shared__ long long s_base[kMaxList];
     const int i = threadIdx.x, lane = threadIdx.x & 31;
     const bool teller = cta_rank() == 0;   // flags and lengths are written once
     pdl_allow_dependents();
@@ -285,7 +285,6 @@ __global__ void __launch_bounds__(kMapThreads)
     s_base[i] = scan & kPages;
     s_last[i] = own_copy ? last : -1;
     s_slot[i] = (int)(scan >> 40);
-    if (i == 0) s_base[kMaxList] = total;
 
     int before, all;
     rank_free(c, span, ahead, &before, &all);
