@@ -541,7 +541,7 @@ int tp_mlp_copy_async(void *dst, const void *src, size_t bytes, tp_mlp_stream_t 
  *
  * Order: calls that change the map or the pages must not overlap other calls
  * on the same cache (one stream, or events); attention calls may overlap each
- * other.  Every call may be captured in a CUDA graph.  Inputs, outputs and
+ * other.  Every call that takes a stream may be captured in a CUDA graph.  Inputs, outputs and
  * workspaces must not overlap the cache's buffers or each other.
  */
 typedef struct {

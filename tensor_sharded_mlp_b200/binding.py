@@ -42,7 +42,8 @@ class Kv8Cache(ctypes.Structure):
     """tp_mlp_kv8_cache: the paged 8-bit key/value cache's buffers and sizes."""
     _fields_ = [(_n, _vp) for _n in ("k", "v", "k_scale", "v_scale", "table", "lengths", "refcount", "status")] + \
                [(_n, _i) for _n in ("layers", "num_pages", "kv_heads", "page_size", "head_dim", "max_seqs", "max_pages")]
-    pages_workspace = None   # bytes, once asked for
+    pages_workspace = None       # bytes, once asked for
+    attention_workspace = None
 
 
 _kv8 = ctypes.POINTER(Kv8Cache)
@@ -431,12 +432,14 @@ def _here(t: torch.Tensor) -> bool:
 def _scratch(nbytes: int, stream) -> torch.Tensor:
     """Device scratch for one call: torch hands the memory out again only to
     work behind the call (under capture it belongs to the graph)."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    if isinstance(stream, torch.cuda.Stream):
-        ws.record_stream(stream)
-    elif stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(int(stream)))
-    return ws
+    return _made_for(torch.empty(nbytes, dtype=torch.uint8, device="cuda"), stream)
+
+
+def _made_for(t: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor allocated on the current stream for a call on `stream` (None: the same)."""
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return t
 
 
 def _rows(t: torch.Tensor, what: str, dims: int, heads: int, head_dim: int) -> int:
@@ -541,9 +544,11 @@ def _kv8_query(cache: Kv8Cache, q: torch.Tensor, seqs, positions):
     return n, q_len, heads, stride
 
 
-def _kv8_workspace(cache: Kv8Cache, n: int, q_len: int, heads: int, stream) -> Optional[torch.Tensor]:
-    nbytes = int(_lib.tp_mlp_kv8_attention_workspace_bytes(cache, n, q_len, heads))
-    return _scratch(nbytes, stream) if nbytes else None   # 0: sizes that the call itself refuses
+def _kv8_workspace(cache: Kv8Cache, stream) -> torch.Tensor:
+    # the same for every call on the cache (it holds pieces of rows for each SM)
+    if cache.attention_workspace is None:
+        cache.attention_workspace = int(_lib.tp_mlp_kv8_attention_workspace_bytes(cache, 1, 1, cache.kv_heads))
+    return _scratch(cache.attention_workspace, stream)
 
 
 def _dense(t: torch.Tensor, shape, dtype, what: str) -> torch.Tensor:
@@ -557,12 +562,12 @@ def tp_mlp_kv8_attention(cache: Kv8Cache, layer: int, q: torch.Tensor, scale: fl
                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of q (n, q_len, heads, head_dim) over one layer of the cache."""
     n, q_len, heads, stride = _kv8_query(cache, q, seqs, positions)
-    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else \
+    out = _made_for(torch.empty_like(q, memory_format=torch.contiguous_format), stream) if out is None else \
         _dense(out, q.shape, q.dtype, "out")
-    ws = _kv8_workspace(cache, n, q_len, heads, stream)
+    ws = _kv8_workspace(cache, stream)
     _check("tp_mlp_kv8_attention",
            _lib.tp_mlp_kv8_attention(cache, layer, _ptr(q), stride, _ptr(seqs), _ptr(positions), n, q_len, heads,
-                                     float(scale), _kv8_dtype(q), _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
+                                     float(scale), _kv8_dtype(q), _ptr(out), _ptr(ws), ws.numel(),
                                      _stream(stream)))
     return out
 
@@ -577,17 +582,17 @@ def tp_mlp_kv8_attention_partials(cache: Kv8Cache, layer: int, q: torch.Tensor, 
 
     def stat(t, what):
         if t is None:
-            return q.new_empty(q.shape[:3], dtype=torch.float32)
+            return _made_for(q.new_empty(q.shape[:3], dtype=torch.float32), stream)
         return _dense(t, q.shape[:3], torch.float32, what)
 
     maximum, exp_sum = stat(maximum, "maximum"), stat(exp_sum, "exp_sum")
-    weighted = torch.empty_like(q, memory_format=torch.contiguous_format) if weighted is None else \
+    weighted = _made_for(torch.empty_like(q, memory_format=torch.contiguous_format), stream) if weighted is None else \
         _dense(weighted, q.shape, q.dtype, "weighted")
-    ws = _kv8_workspace(cache, n, q_len, heads, stream)
+    ws = _kv8_workspace(cache, stream)
     _check("tp_mlp_kv8_attention_partials",
            _lib.tp_mlp_kv8_attention_partials(cache, layer, _ptr(q), stride, _ptr(seqs), _ptr(positions), n, q_len,
                                               heads, float(scale), _kv8_dtype(q), _ptr(maximum), _ptr(exp_sum),
-                                              _ptr(weighted), _ptr(ws), 0 if ws is None else ws.numel(),
+                                              _ptr(weighted), _ptr(ws), ws.numel(),
                                               _stream(stream)))
     return maximum, exp_sum, weighted
 

@@ -68,6 +68,9 @@ class KvCache8:
         self.layers, self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.device = k.device
         self.c = binding.Kv8Cache(*(ctypes.c_void_p(t.data_ptr()) for t in tensors), *k.shape, *table.shape)
+        if binding._lib.tp_mlp_kv8_pages_workspace_bytes(self.c) == 0:
+            raise ValueError("page_size must be 16, 32, 64, 128 or 256, head_dim 64, 128 or 256, kv_heads at most 256, "
+                             "and every size at least 1")
 
     def _on(self):
         if binding._current_device() != self.device.index:
@@ -109,7 +112,7 @@ class KvCache8:
     def compact(self, new_index: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Returns the new number of every page (-1 for pages that were free)."""
         if new_index is None:
-            new_index = torch.empty(self.num_pages, dtype=torch.int32, device=self.device)
+            new_index = binding._made_for(torch.empty(self.num_pages, dtype=torch.int32, device=self.device), stream)
         binding.tp_mlp_kv8_compact(self._on(), new_index, stream)
         return new_index
 

@@ -77,6 +77,25 @@ def test_several_queries_are_causal(q_len, kv_heads, group, dtype):
     check(c, on_gpu(c), query(r, len(lengths), q_len, kv_heads * group, 64, dtype), list(range(len(lengths))))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("head_dim", [128, 256])
+@pytest.mark.parametrize("q_len,kv_heads,group", [(5, 1, 3), (2, 2, 8), (9, 1, 5)])
+def test_several_queries_of_wider_heads(q_len, kv_heads, group, head_dim, dtype):
+    r = np.random.default_rng(q_len + head_dim)
+    lengths = [q_len - 1, q_len + 14, 100, 40]
+    c = filled(r, lengths, 1, kv_heads, 32, head_dim)
+    check(c, on_gpu(c), query(r, 4, q_len, kv_heads * group, head_dim, dtype), [3, 2, 1, 0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_short_segments_beside_a_long_one(dtype):
+    """Sequences of one step each, and one of hundreds: every way a segment's start and end can meet a cut."""
+    r = np.random.default_rng(30)
+    lengths = [int(x) for x in r.integers(0, 20, 120)] + [5000] + [int(x) for x in r.integers(0, 70, 60)]
+    c = filled(r, lengths, 1, 2, 16, 64)
+    check(c, on_gpu(c), query(r, len(lengths), 1, 6, 64, dtype), list(range(len(lengths))))
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 def test_page_sizes_and_layers(page):
     r = np.random.default_rng(page)
@@ -278,9 +297,65 @@ def test_same_result_every_time_and_on_another_stream():
     out = torch.empty_like(q)
     torch.cuda.synchronize()
     cache.attention(0, q, seqs, out=out, stream=streams[0])
+    outs += [out, cache.attention(0, q, seqs, stream=streams[1]), cache.attention(0, q, seqs, stream=streams[2].cuda_stream)]
     torch.cuda.synchronize()
-    for o in outs + [out]:
+    for o in outs:
         assert torch.equal(o, first)
+
+
+def test_two_caches_at_once():
+    """Steps of two caches on two streams, page work and attention among each other's."""
+    from tensor_sharded_mlp_b200 import kv_cache
+    r = np.random.default_rng(31)
+    caches, oracles, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(2):
+        caches.append(kv_cache.KvCache8(1, 64, 2, 64, page_size=16, max_seqs=4, max_tokens=256))
+        oracles.append(kv8.new_cache(1, 64, 2, 16, 64, 4, 16))
+    seqs, counts = ints([0, 1, 2, 3]), ints([7] * 4)
+    rows = [[tuple(torch.from_numpy(r.standard_normal((28, 2, 64)).astype(np.float32)).cuda() for _ in range(2)) for _ in range(2)]
+            for _ in range(6)]
+    q = query(r, 4, 2, 4, 64, "f32")
+    torch.cuda.synchronize()
+    got = [None, None]
+    for step in range(6):
+        for x in range(2):
+            with torch.cuda.stream(streams[x]):
+                caches[x].reserve(seqs, counts)
+                caches[x].append(0, *rows[step][x], seqs)
+                got[x] = caches[x].attention(0, q, seqs)
+    torch.cuda.synchronize()
+    for x in range(2):
+        c = oracles[x]
+        for step in range(6):
+            kv8.reserve(c, range(4), [7] * 4)
+            kv8.append(c, 0, *(t.double().cpu().numpy() for t in rows[step][x]), range(4), [0, 7, 14, 21, 28])
+        np.testing.assert_array_equal(caches[x].table.cpu().numpy(), c["table"])
+        want, reach, vmax = kv8.attention(c, 0, q.double().cpu().numpy(), range(4), 0.125)
+        rel = weight_bound(reach, 64, 42, torch.float32)
+        close(got[x], want, rel * vmax + HALF[torch.float32] * np.abs(want), f"cache {x}")
+        caches[x].check()
+
+
+def test_sizes_are_refused_when_the_cache_is_made():
+    from tensor_sharded_mlp_b200 import kv_cache
+    for over in (dict(page_size=24), dict(head_dim=96), dict(page_size=512), dict(kv_heads=300)):
+        with pytest.raises(ValueError):
+            kv_cache.KvCache8(**{**dict(layers=1, num_pages=4, kv_heads=1, head_dim=64, page_size=16, max_seqs=1,
+                                        max_tokens=64), **over})
+    c = kv_cache.KvCache8(1, 4, 1, 64, page_size=16, max_seqs=1, max_tokens=64)
+    with pytest.raises(ValueError):
+        kv_cache.KvCache8.over(c.k, c.v, c.k_scale, c.v_scale, c.table.long(), c.lengths, c.refcount, c.status)
+    with pytest.raises(ValueError):
+        kv_cache.KvCache8.over(c.k, c.v, c.k_scale, c.v_scale, c.table, c.lengths, c.refcount[:3], c.status)
+
+
+def test_check_raises_and_clears():
+    c = filled(np.random.default_rng(32), [5, 6])
+    cache = on_gpu(c)
+    cache.truncate(ints([0, 7]), ints([9, 0]))
+    with pytest.raises(RuntimeError, match="BAD_SEQUENCE, BAD_LENGTH"):
+        cache.check()
+    cache.check()
 
 
 def test_offsets_beyond_32_bits():
