@@ -16,8 +16,6 @@
 // chain of dependent loads in front of the rows (lists, length, page, refcount)
 // is walked once for all of them.  For a decode step that chain is all there
 // is: a warp takes a unit, and the rows are loaded beside the page's refcount.
-#include <float.h>
-
 #include "common.cuh"
 #include "internal.h"
 #include "kv8.cuh"
@@ -30,11 +28,24 @@ constexpr int kKeep = 4;    // vectors of 8 elements of keys (and of values) a t
 constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
 constexpr int kMaxSlots = 34;
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Eight consecutive elements as loaded.
 template <typename T> struct Vec8;
 template <> struct Vec8<__nv_bfloat16> {
     uint4 u;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = ld_stream_v4(p); }
+    // largest magnitude so far, as bits that compare like the numbers (infinities and NaN on top): two at a time
+    using Most = uint32_t;
+    __device__ __forceinline__ void raise(Most &m) const {
+        m = max_u16x2(max_u16x2(m, u.x & 0x7fff7fffu), max_u16x2(u.y & 0x7fff7fffu, u.z & 0x7fff7fffu));
+        m = max_u16x2(m, u.w & 0x7fff7fffu);
+    }
+    static __device__ __forceinline__ uint32_t bits(Most m) { return max(m & 0xffffu, m >> 16) << 16; }
     __device__ __forceinline__ void widen(float (&f)[8]) const {
         f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
         f[4] = bf16lo(u.z); f[5] = bf16hi(u.z); f[6] = bf16lo(u.w); f[7] = bf16hi(u.w);
@@ -43,6 +54,13 @@ template <> struct Vec8<__nv_bfloat16> {
 template <> struct Vec8<float> {
     uint4 u, w;
     __device__ __forceinline__ void load(const float *p) { u = ld_stream_v4(p); w = ld_stream_v4(p + 4); }
+    using Most = uint32_t;
+    __device__ __forceinline__ void raise(Most &m) const {
+        const uint32_t a = max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu));
+        const uint32_t b = max(max(w.x & 0x7fffffffu, w.y & 0x7fffffffu), max(w.z & 0x7fffffffu, w.w & 0x7fffffffu));
+        m = max(m, max(a, b));
+    }
+    static __device__ __forceinline__ uint32_t bits(Most m) { return m; }
     __device__ __forceinline__ void widen(float (&f)[8]) const {
         f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
         f[4] = __uint_as_float(w.x); f[5] = __uint_as_float(w.y); f[6] = __uint_as_float(w.z); f[7] = __uint_as_float(w.w);
@@ -50,45 +68,40 @@ template <> struct Vec8<float> {
 };
 
 // 2^ceil(log2(amax / 448)), at least 2^-100, from amax's bits: 448 = 1.75 * 2^8.
-__device__ __forceinline__ float step_of(float amax) {
-    const uint32_t b = __float_as_uint(amax);
+__device__ __forceinline__ float step_of(uint32_t b) {
     int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
     e = e < -100 ? -100 : e;   // (zero and subnormal maxima land here)
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ float finite_max(float m, float x) {
-    const float a = fabsf(x);
-    return a <= FLT_MAX ? fmaxf(m, a) : m;
-}
-
 // Maxima over the group of G threads that works on one unit; `turn` alternates between calls.
 template <int G>
-__device__ __forceinline__ float2 group_max(float2 m, int turn) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
-        m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
-    }
+__device__ __forceinline__ uint2 group_max(uint32_t x, uint32_t y, int turn) {
+    uint2 m = make_uint2(__reduce_max_sync(0xffffffffu, x), __reduce_max_sync(0xffffffffu, y));
     if (G > 32) {
-        __shared__ float2 part[2][kThreads / 32];   // (two: a warp may be a call ahead of one that still reads)
+        __shared__ uint2 part[2][kThreads / 32];   // (two: a warp may be a call ahead of one that still reads)
         if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = m;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            m.x = fmaxf(m.x, part[turn][w].x);
-            m.y = fmaxf(m.y, part[turn][w].y);
+            m.x = max(m.x, part[turn][w].x);
+            m.y = max(m.y, part[turn][w].y);
         }
     }
     return m;
 }
 
+// The largest finite magnitude of a vector's elements (the rows hold infinities or NaN).
 template <typename T>
-__device__ __forceinline__ void take_max(const Vec8<T> &r, float &m) {
+__device__ __forceinline__ uint32_t finite_max(const Vec8<T> &r, uint32_t m) {
     float f[8];
     r.widen(f);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) m = finite_max(m, f[q]);
+    for (int q = 0; q < 8; ++q) {
+        const uint32_t b = __float_as_uint(f[q]) & 0x7fffffffu;
+        m = b < 0x7f800000u ? max(m, b) : m;
+    }
+    return m;
 }
 
 template <typename T>
@@ -215,21 +228,33 @@ __device__ __forceinline__ void append_unit(const Kv8 &c, const T *k, const T *v
     const long long where = (long long)sl.page * c.kv_heads + head;
     // read by all threads before one of them writes it: the maxima's exchange lies between
     const float old_k = a ? c.k_scale[where] : 0.f, old_v = a ? c.v_scale[where] : 0.f;
-    float2 amax = make_float2(0.f, 0.f);
+    typename Vec8<T>::Most most_k = 0, most_v = 0;
 #pragma unroll
     for (int x = 0; x < kKeep; ++x)
         if (me + x * G < vecs) {
-            take_max(kk[x], amax.x);
-            take_max(kv[x], amax.y);
+            kk[x].raise(most_k);
+            kv[x].raise(most_v);
         }
     for (int e = me + kKeep * G; e < vecs; e += G) {
         Vec8<T> r, w;
         r.load(k + at(e));
         w.load(v + at(e));
-        take_max(r, amax.x);
-        take_max(w, amax.y);
+        r.raise(most_k);
+        w.raise(most_v);
     }
-    amax = group_max<G>(amax, turn);
+    uint2 amax = group_max<G>(Vec8<T>::bits(most_k), Vec8<T>::bits(most_v), turn);
+    if (max(amax.x, amax.y) >= 0x7f800000u) {   // only the finite ones count (the whole group is here)
+        uint32_t fk = 0, fv = 0;
+        for (int e = me; e < vecs; e += G) {
+            Vec8<T> r, w;
+            r.load(k + at(e));
+            w.load(v + at(e));
+            fk = finite_max(r, fk);
+            fv = finite_max(w, fv);
+        }
+        if (G > 32) __syncthreads();   // (everyone has read the exchange's last values)
+        amax = group_max<G>(fk, fv, turn);
+    }
     const float scale_k = a ? fmaxf(old_k, step_of(amax.x)) : step_of(amax.x);
     const float scale_v = a ? fmaxf(old_v, step_of(amax.y)) : step_of(amax.y);
     const float inv_k = 1.f / scale_k, inv_v = 1.f / scale_v;   // exact for powers of two
