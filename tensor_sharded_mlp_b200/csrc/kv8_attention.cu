@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const long long c0 = first_step(blockIdx.x), c1 = first_step(blockIdx.x + 1);
     const long long w0 = c0 + (c1 - c0) * warp / C::kWarps, w1 = c0 + (c1 - c0) * (warp + 1) / C::kWarps;
 
-    // 2. this warp's steps, segment by segment.  The loads run kStages - 1 steps ahead of the products, across segments.
+    // 2. this warp's steps, segment by segment.  The loads run a ring ahead of the products, across segments.
     int e = 0, unit = 0, n_pieces = 0;
     if (w0 < w1) e = entry_of(prefix, n, w0);
     const int page_steps = c.page_shift - 4;            // log2(steps of a page)
@@ -725,9 +725,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(f[i]));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-                ex = ex > 127 ? 0 : max(ex, -126);   // an infinite row stays as it is
-                const float down = ex == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - ex) << 23);   // 2^-ex
+                const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 127);
+                const float down = amax > FLT_MAX ? NAN   // an infinity in a row makes its scores, and so its result, NaN
+                                   : ex == 127    ? 0x1p-127f
+                                                  : __uint_as_float((uint32_t)(127 - ex) << 23);   // 2^-ex
 #pragma unroll
                 for (int k = 0; k < kKs; ++k) {
 #pragma unroll
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
             // steps below `plain` need no mask: the tile's first row sees the fewest tokens
             plain = en.seen(map.query(tile * C::kRows)) / kStep;
-            #pragma unroll
+#pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int m = 0; m < kMt; ++m)

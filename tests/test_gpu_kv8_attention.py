@@ -213,6 +213,16 @@ def test_nan_queries_stay_in_their_rows():
     want = torch.zeros_like(bad)
     want[0, 1, 3], want[1, 0, 5] = True, True
     assert torch.equal(bad, want) and torch.isfinite(out[~want]).all()
+    # one token: a score of minus infinity is no unseen token
+    for dtype in ("bf16", "f32"):
+        c = filled(r, [1, 0], 1, 1, 16, 64)
+        q = query(r, 2, 1, 3, 64, dtype)
+        q[:, 0, 0, 5], q[:, 0, 1, 5] = float("inf"), float("-inf")
+        cache = on_gpu(c)
+        out = cache.attention(0, q, ints([0, 1])).float()
+        m, l, w = cache.attention_partials(0, q, ints([0, 1]))
+        assert all(torch.isnan(t[0, 0, :2]).all() and torch.isfinite(t[0, 0, 2]).all() for t in (out, m, l, w.float()))
+        assert not out[1].bool().any() and torch.isneginf(m[1]).all() and not l[1].bool().any()
 
 
 def test_small_and_large_queries():
