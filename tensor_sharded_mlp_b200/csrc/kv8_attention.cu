@@ -696,10 +696,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     e4m3_to_f16(__byte_perm(v[0][i], v[1][i], sel), a0, a1);
                     e4m3_to_f16(__byte_perm(v[2][i], v[3][i], sel), a2, a3);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (!kExact) {
+                            mma(o[nt][2 * i + h], a0, a1, a2, a3, w[y][0][nt][0], w[y][0][nt][1]);
+                        } else {
+                            // the mma's own sum cuts what it shifts out: over thousands of steps that adds up, so for
+                            // fp32 results a step's sum is added by an instruction that rounds
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma(d, a0, a1, a2, a3, w[y][0][nt][0], w[y][0][nt][1]);
+                            mma(d, a0, a1, a2, a3, w[y][kParts - 1][nt][0], w[y][kParts - 1][nt][1]);
 #pragma unroll
-                        for (int pt = 0; pt < kParts; ++pt)
-                            mma(o[nt][2 * i + h], a0, a1, a2, a3, w[y][pt][nt][0], w[y][pt][nt][1]);
+                            for (int k = 0; k < 4; ++k) o[nt][2 * i + h][k] += d[k];
+                        }
+                    }
                 }
         }
     };
