@@ -567,7 +567,9 @@ typedef enum {
     TP_MLP_KV8_BAD_PAGE = 4,     /* a page number outside the pool                           */
     TP_MLP_KV8_NO_PAGES = 8,     /* too few free pages: the whole tp_mlp_kv8_reserve call
                                     changed nothing                                          */
-    TP_MLP_KV8_SHARED_PAGE = 16  /* an append met a page that other sequences hold too       */
+    TP_MLP_KV8_SHARED_PAGE = 16, /* an append met a page that other sequences hold too       */
+    TP_MLP_KV8_TIMEOUT = 32      /* a wait inside an attention kernel gave up: the call's
+                                    results are not valid                                    */
 } tp_mlp_kv8_flag;
 
 /* Most sequences (or page pairs) in one call's list. */

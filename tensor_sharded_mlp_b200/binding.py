@@ -43,13 +43,13 @@ class Kv8Cache(ctypes.Structure):
     _fields_ = [(_n, _vp) for _n in ("k", "v", "k_scale", "v_scale", "table", "lengths", "refcount", "status")] + \
                [(_n, _i) for _n in ("layers", "num_pages", "kv_heads", "page_size", "head_dim", "max_seqs", "max_pages")]
     pages_workspace = None       # bytes, once asked for
-    attention_workspace = None
+    attention_workspace = (0, 0, 0)       # bytes for the (q_len, heads) of the last call
 
 
 _kv8 = ctypes.POINTER(Kv8Cache)
 _ll = ctypes.c_longlong
 KV8_MAX_LIST = 1024
-KV8_FLAGS = {1: "BAD_SEQUENCE", 2: "BAD_LENGTH", 4: "BAD_PAGE", 8: "NO_PAGES", 16: "SHARED_PAGE"}
+KV8_FLAGS = {1: "BAD_SEQUENCE", 2: "BAD_LENGTH", 4: "BAD_PAGE", 8: "NO_PAGES", 16: "SHARED_PAGE", 32: "TIMEOUT"}
 
 _SIGS = {
     "tp_mlp_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i, _i, _i, _i]),
@@ -544,11 +544,11 @@ def _kv8_query(cache: Kv8Cache, q: torch.Tensor, seqs, positions):
     return n, q_len, heads, stride
 
 
-def _kv8_workspace(cache: Kv8Cache, stream) -> torch.Tensor:
-    # the same for every call on the cache (it holds pieces of rows for each SM)
-    if cache.attention_workspace is None:
-        cache.attention_workspace = int(_lib.tp_mlp_kv8_attention_workspace_bytes(cache, 1, 1, cache.kv_heads))
-    return _scratch(cache.attention_workspace, stream)
+def _kv8_workspace(cache: Kv8Cache, q_len: int, heads: int, stream) -> torch.Tensor:
+    # (it holds pieces of rows for each SM: the same for any n and any history)
+    if cache.attention_workspace[:2] != (q_len, heads):
+        cache.attention_workspace = (q_len, heads, int(_lib.tp_mlp_kv8_attention_workspace_bytes(cache, 1, q_len, heads)))
+    return _scratch(cache.attention_workspace[2], stream)
 
 
 def _dense(t: torch.Tensor, shape, dtype, what: str) -> torch.Tensor:
@@ -564,7 +564,7 @@ def tp_mlp_kv8_attention(cache: Kv8Cache, layer: int, q: torch.Tensor, scale: fl
     n, q_len, heads, stride = _kv8_query(cache, q, seqs, positions)
     out = _made_for(torch.empty_like(q, memory_format=torch.contiguous_format), stream) if out is None else \
         _dense(out, q.shape, q.dtype, "out")
-    ws = _kv8_workspace(cache, stream)
+    ws = _kv8_workspace(cache, q_len, heads, stream)
     _check("tp_mlp_kv8_attention",
            _lib.tp_mlp_kv8_attention(cache, layer, _ptr(q), stride, _ptr(seqs), _ptr(positions), n, q_len, heads,
                                      float(scale), _kv8_dtype(q), _ptr(out), _ptr(ws), ws.numel(),
@@ -582,13 +582,13 @@ def tp_mlp_kv8_attention_partials(cache: Kv8Cache, layer: int, q: torch.Tensor, 
 
     def stat(t, what):
         if t is None:
-            return _made_for(q.new_empty(q.shape[:3], dtype=torch.float32), stream)
-        return _dense(t, q.shape[:3], torch.float32, what)
+            return _made_for(torch.empty(n, q_len, heads, dtype=torch.float32, device=q.device), stream)
+        return _dense(t, (n, q_len, heads), torch.float32, what)
 
     maximum, exp_sum = stat(maximum, "maximum"), stat(exp_sum, "exp_sum")
     weighted = _made_for(torch.empty_like(q, memory_format=torch.contiguous_format), stream) if weighted is None else \
         _dense(weighted, q.shape, q.dtype, "weighted")
-    ws = _kv8_workspace(cache, stream)
+    ws = _kv8_workspace(cache, q_len, heads, stream)
     _check("tp_mlp_kv8_attention_partials",
            _lib.tp_mlp_kv8_attention_partials(cache, layer, _ptr(q), stride, _ptr(seqs), _ptr(positions), n, q_len,
                                               heads, float(scale), _kv8_dtype(q), _ptr(maximum), _ptr(exp_sum),

@@ -125,7 +125,7 @@ int attention(const tp_mlp_kv8_cache *cache, int layer, const Kv8Query &a, bool 
     if ((s = check_list(a.seqs, a.n, true)) || (s = check_list(a.positions, a.n, true))) return s;
     int sms = 0;
     if ((s = sm_count(&sms))) return s;
-    const size_t need = kv8_attention_workspace(c, sms);
+    const size_t need = kv8_attention_workspace(c, a.q_len, a.heads, sms);
     if (!ws || ws_bytes < need) return TP_MLP_ERR_WORKSPACE;
     if ((s = check_dev(ws, need))) return s;
     to_layer(&c, layer);
@@ -256,7 +256,7 @@ size_t tp_mlp_kv8_attention_workspace_bytes(const tp_mlp_kv8_cache *cache, int n
         cudaGetLastError();
         sms = 148;   // B200
     }
-    return kv8_attention_workspace(c, sms);
+    return kv8_attention_workspace(c, q_len, heads, sms);
 }
 
 int tp_mlp_kv8_attention(const tp_mlp_kv8_cache *cache, int layer, const void *q, long long row_stride,
