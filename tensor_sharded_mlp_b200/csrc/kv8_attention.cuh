@@ -357,16 +357,21 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // Eight warps a row where a segment has many pieces, four (half as many CTAs) otherwise: one sequence of 200000 tokens with
 // one KV head 26.3 against 30.8 us, of 20000 with two 14.5 / 17.2, of 4099 with eight 12.0 / 12.3; 16 sequences of 4000 with
-// eight (128 segments) 32.7 / 31.9, 32 ragged ones 44.8 / 44.0.
+// eight (128 segments) 32.7 / 31.9, 32 ragged ones 44.8 / 44.0.  One warp a row of the wide tiles, where the rows are many
+// (128 rows of head_dim 128; 1 / 2 / 4 warps a row): 16 sequences of 4000 tokens 98 / 101 / 109 us, one 28.2 / 27.4 / 29.9.
 template <typename T, int D, int kRows>
 cudaError_t launch_combine(const Kv8 &c, const Kv8Query &a, const Split &s, int row_tiles, int num_sms, cudaStream_t st) {
-    const long long segments = (long long)a.n * c.kv_heads * row_tiles;
     const int join_rows = min(kRows, (a.q_len * (a.heads / c.kv_heads) + 7) / 8 * 8);
-    if (segments * 8 <= num_sms)
-        return launch_pdl(combine_kernel<T, D, kRows, 8>, dim3((unsigned)num_sms, join_rows), dim3(kJoinThreads), 0, st, c, a, s,
-                          row_tiles);
-    return launch_pdl(combine_kernel<T, D, kRows, 4>, dim3((unsigned)num_sms, join_rows / 2), dim3(kJoinThreads), 0, st, c, a, s,
-                      row_tiles);
+    if constexpr (kRows == kWideRows) {
+        return launch_pdl(combine_kernel<T, D, kRows, 1>, dim3((unsigned)num_sms, join_rows / 8), dim3(kJoinThreads), 0, st, c,
+                          a, s, row_tiles);
+    } else {
+        if ((long long)a.n * c.kv_heads * row_tiles * 8 <= num_sms)
+            return launch_pdl(combine_kernel<T, D, kRows, 8>, dim3((unsigned)num_sms, join_rows), dim3(kJoinThreads), 0, st, c,
+                              a, s, row_tiles);
+        return launch_pdl(combine_kernel<T, D, kRows, 4>, dim3((unsigned)num_sms, join_rows / 2), dim3(kJoinThreads), 0, st, c,
+                          a, s, row_tiles);
+    }
 }
 
 inline Split split_of(void *ws, int num_sms) {

@@ -21,13 +21,16 @@
 // The tiles of all segments are cut evenly over the CTAs as in kv8_attention.cu, and the same kernel joins pieces.  Every
 // wait is bounded; one that gives up ends the CTA and sets TP_MLP_KV8_TIMEOUT.
 //
-// Measured (B200, 16 sequences of 4000 tokens, 8 KV heads; this kernel against kv8_attention.cu's, us): head_dim 128, 128
-// rows MEAS.
-// What bounds it: a tile takes some 4300 cycles (of 128 tokens, 32 KB), of which the products keep the tensor pipe busy for
-// 19 %; the way of a tile through the two places of keys and values (store 1700, scores 1000, softmax 3300, outputs
-// 1000 cycles, each with a barrier's latency) is what repeats.  Tried beside this form: keys' and values' places freed
-// separately, 99-153 us against 95 at 64 rows (more code, and the loaders' in-order warps then bound it); two threads a
-// row 113; 16 loading warps 99-113; weights through shared memory 105.
+// Measured (B200, bf16, 8 KV heads, 16 sequences of 4000 tokens; kv8_attention.cu's kernel -> this one, us):
+//   rows            72            128            256           1024
+//   head_dim 64   103 -> 75     132 -> 80      244 -> 142     914 -> 507
+//   head_dim 128  144 -> 92     220 -> 98      429 -> 174    1652 -> 623
+//   head_dim 256  294 -> 155    606 -> 165    1243 -> 297    4912 -> 1068
+// What bounds it: a tile's way through the two places of keys and values (some 4300 cycles for 128 tokens of 128 columns:
+// codes to operands 1700, scores 1000, softmax 3300, outputs 1000, each behind a barrier; two tiles are on it at a time).
+// The tensor pipe is busy 19 % of the time.  Tried beside this form (64 rows of head_dim 128, 95 us): weights through shared
+// memory 105; keys' and values' places freed separately 99-153, the more the longer the unrolled code; two threads a row
+// 113; 16 loading warps 99-113.
 #include "kv8_attention.cuh"
 
 namespace tpmlp {
@@ -563,9 +566,12 @@ cudaError_t launch_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, 
 
 }  // namespace
 
-// From where on it gains: RULE
+// From where on the products bound the other kernel.  At 64 rows a long history gains here (head_dim 64 / 128 / 256: 75 -> 78,
+// 118 -> 90, 292 -> 154 us) and a short one loses: a segment's queries, outputs and join cost more (one sequence of 4000
+// tokens: 72 rows 22 -> 22, 20 -> 25, 38 -> 40 us; 128 rows 24 -> 25, 25 -> 28, 45 -> 48; 8 of 100 to 300 tokens, 128 rows:
+// 21 -> 18, 20 -> 22, 29 -> 43).
 bool kv8_wide_rows(const Kv8 &c, int q_len, int heads) {
-    return q_len * (heads / c.kv_heads) > (c.head_dim == 256 ? 32 : 64);
+    return q_len * (heads / c.kv_heads) > 64;
 }
 
 bool kv8_wide_fits(const Kv8 &c, const Kv8Query &a) {
