@@ -69,7 +69,6 @@ struct Kv8Query {
 };
 // kv8_attention_wide.cu: the form for many query rows a KV head
 bool kv8_wide_rows(const Kv8 &c, int q_len, int heads);            // whether they are
-bool kv8_wide_fits(const Kv8 &c, const Kv8Query &a);               // ... and the call's type and list
 cudaError_t launch_kv8_attention_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st);
 size_t kv8_attention_workspace(const Kv8 &c, int q_len, int heads, int num_sms);
 cudaError_t launch_kv8_attention(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st);

@@ -783,7 +783,7 @@ size_t kv8_attention_workspace(const Kv8 &c, int q_len, int heads, int num_sms) 
 
 cudaError_t launch_kv8_attention(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
     if (a.dtype == TP_MLP_F32) return launch_typed<float>(c, a, ws, num_sms, st);
-    if (kv8_wide_fits(c, a)) return launch_kv8_attention_wide(c, a, ws, num_sms, st);
+    if (kv8_wide_rows(c, a.q_len, a.heads)) return launch_kv8_attention_wide(c, a, ws, num_sms, st);
     return launch_typed<__nv_bfloat16>(c, a, ws, num_sms, st);
 }
 

@@ -47,10 +47,10 @@ struct WideCfg {
     static constexpr int kScores = 0, kOut = 2 * kTok, kWeights = kOut + D, kColumns = 512;   // TMEM
     static constexpr int kKeys = 0, kValues = 2 * kTile, kQuery = 4 * kTile;
     static constexpr int kScales = kQuery + kWideRows * D * 2, kPrefix = kScales + 2 * (kTok / 16) * 8;
-    static constexpr size_t smem(int n) { return 1024 + kPrefix + (size_t)(n + 1) * 8 + (size_t)n * 16; }
+    static constexpr size_t smem(int n) { return 1024 + (size_t)kPrefix + (size_t)(n + 1) * 8 + (size_t)n * 16; }
     static_assert(kWeights + kTok <= kColumns, "TMEM of an SM");
+    static_assert(smem(kMaxList) <= 226 * 1024, "shared memory of an SM; the static part beside it is below 1 KB");
 };
-constexpr size_t kWideSmem = 226 * 1024;    // dynamic; the static part beside it is below 1 KB
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
     asm volatile(
@@ -557,7 +557,7 @@ cudaError_t launch_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, 
     const int row_tiles = (a.q_len * (a.heads / c.kv_heads) + kWideRows - 1) / kWideRows;
     const Split s = split_of(ws, num_sms);
     auto kern = attention_wide_kernel<D>;
-    cudaError_t e = ensure_smem_attr(kern, kWideSmem);
+    cudaError_t e = ensure_smem_attr(kern, C::smem(kMaxList));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)num_sms), dim3(C::kThreads), C::smem(a.n), st, c, a, s, row_tiles);
     if (e != cudaSuccess) return e;
@@ -572,12 +572,6 @@ cudaError_t launch_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, 
 // 21 -> 18, 20 -> 22, 29 -> 43).
 bool kv8_wide_rows(const Kv8 &c, int q_len, int heads) {
     return q_len * (heads / c.kv_heads) > 64;
-}
-
-bool kv8_wide_fits(const Kv8 &c, const Kv8Query &a) {
-    const size_t smem = c.head_dim == 64 ? WideCfg<64>::smem(a.n) : c.head_dim == 128 ? WideCfg<128>::smem(a.n)
-                                                                                      : WideCfg<256>::smem(a.n);
-    return a.dtype == TP_MLP_BF16 && kv8_wide_rows(c, a.q_len, a.heads) && smem <= kWideSmem;
 }
 
 cudaError_t launch_kv8_attention_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
