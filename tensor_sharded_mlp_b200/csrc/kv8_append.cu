@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "kv8.cuh"
+#include "kv8_run.h"
 
 namespace tpmlp {
 namespace {
@@ -81,7 +82,7 @@ __device__ __forceinline__ float step_of(uint32_t b) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Maxima over the group of G threads that works on one unit; `turn` alternates between calls.
+// Maxima over the group of G threads that works on one unit; `turn` alternates between the units of a CTA (for_units).
 template <int G>
 __device__ __forceinline__ uint2 group_max(uint32_t x, uint32_t y, int turn) {
     uint2 m = make_uint2(__reduce_max_sync(0xffffffffu, x), __reduce_max_sync(0xffffffffu, y));
@@ -339,14 +340,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         if ((threadIdx.x & 31) == 0) s_slot[x] = sl;
     }
     __syncthreads();
-    int x = 0, head = head0;
-    for (int u = 0; u < run; ++u) {
-        if (s_slot[x].page >= 0) append_unit<T, kThreads>(c, k, v, row_stride, s_slot[x], head, true, u & 1);
-        if (++head == c.kv_heads) {
-            head = 0;
-            ++x;
-        }
-    }
+    for_units(
+        run, head0, c.kv_heads, [&](int x) { return s_slot[x].page >= 0; },
+        [&](int x, int head, int turn) { append_unit<T, kThreads>(c, k, v, row_stride, s_slot[x], head, true, turn); });
 }
 
 template <typename T>

@@ -194,3 +194,49 @@ def test_wrappers_refuse_host_tensors(b):
                  lambda: b.tp_mlp_kv8_attention(c, 0, torch.zeros(1, 1, 2, 64), 1.0)):
         with pytest.raises(ValueError):
             call()
+
+
+# --- the order of a CTA's units in the prompt append --------------------------------------------------------------------
+
+RUN_PROGRAM = r"""
+#include <cstdio>
+#include "kv8_run.h"
+int main() {   // heads head0 run bits: the slots with something to write -> "slot head turn" of each unit that runs
+    int heads, head0, run;
+    unsigned long long bits;
+    while (std::scanf("%d %d %d %llu", &heads, &head0, &run, &bits) == 4) {
+        tpmlp::for_units(run, head0, heads, [&](int s) { return (bits >> s & 1) != 0; },
+                         [&](int s, int h, int t) { std::printf("%d %d %d ", s, h, t); });
+        std::printf("\n");
+    }
+}
+"""
+
+
+def test_units_that_follow_each_other_use_two_buffers(tmp_path):
+    """Every unit with something to write runs once, in order, and no two in a row take the same exchange buffer: empty
+    slots (which odd kv_heads make an odd number of skipped units) must not bring two of the same turn together."""
+    import itertools
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("g++") or shutil.which("c++")
+    if cc is None:
+        pytest.skip("no host compiler")
+    src = tmp_path / "run.cpp"
+    src.write_text(RUN_PROGRAM)
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "tensor_sharded_mlp_b200", "csrc")
+    subprocess.run([cc, "-std=c++17", "-I", csrc, str(src), "-o", str(tmp_path / "run")], check=True)
+    cases = []
+    for heads, bits in itertools.product((1, 2, 3, 5, 8), range(64)):
+        for head0 in {0, heads // 2, heads - 1}:
+            for run in (1, heads, 6 * heads - head0):
+                cases.append((heads, head0, run, bits))
+    out = subprocess.run([str(tmp_path / "run")], input="\n".join(" ".join(map(str, x)) for x in cases), text=True,
+                         capture_output=True, check=True).stdout.split("\n")
+    for (heads, head0, run, bits), line in zip(cases, out):
+        got = np.array(line.split(), int).reshape(-1, 3)
+        units = [divmod(head0 + u, heads) for u in range(run)]
+        assert [tuple(x) for x in got[:, :2]] == [x for x in units if bits >> x[0] & 1], (heads, head0, run, bits)
+        assert (got[1:, 2] != got[:-1, 2]).all(), (heads, head0, run, bits)
+        assert set(got[:, 2]) <= {0, 1}
