@@ -657,7 +657,9 @@ int tp_mlp_kv8_compact(const tp_mlp_kv8_cache *cache, int *new_index, void *work
  *              a row every row_stride elements (>= kv_heads * head_dim; a row
  *              starts on a 16-byte boundary)
  *   seqs       device, n ints (NULL: sequence i); each sequence once
- *   cu_tokens  device, n + 1 ints, ascending from 0, or NULL
+ *   cu_tokens  device, n + 1 ints, ascending from 0, or NULL.  An entry whose two bounds are below an earlier bound
+ *              or 0, in falling order or beyond `tokens` is left out and flagged (TP_MLP_KV8_BAD_LENGTH); rows that
+ *              no entry has (those behind cu_tokens[n] of a padded input) are not looked at
  * n <= TP_MLP_KV8_MAX_LIST, tokens <= 4194304; without cu_tokens, tokens % n
  * == 0 (TP_MLP_ERR_SHAPE).  tokens == 0 or n == 0 is a no-op.
  */

@@ -197,9 +197,10 @@ def compact(c):
 def append(c, layer, k, v, seqs, cu):
     page = c["k"].shape[3]
     entries, flags = _entries(c, seqs)
+    before = np.maximum.accumulate(np.concatenate([[0], cu]))      # the largest bound in front of each
     for i, s in entries:
-        n, end = int(cu[i + 1] - cu[i]), int(c["lengths"][s])
-        if n < 0 or cu[i] < 0 or cu[i + 1] > len(k) or end - n < 0 or end > c["table"].shape[1] * page:
+        n, end = int(cu[i + 1]) - int(cu[i]), int(c["lengths"][s])
+        if n < 0 or cu[i] < before[i] or cu[i + 1] > len(k) or end - n < 0 or end > c["table"].shape[1] * page:
             flags |= BAD_LENGTH
             continue
         at, row = end - n, int(cu[i])

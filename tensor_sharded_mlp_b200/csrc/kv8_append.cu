@@ -147,9 +147,10 @@ struct Slot {
 
 // Lists of the call, in shared memory.
 struct Lists {
-    const int *seq, *cu;   // cu NULL: even shares
+    const int *seq, *cu;   // cu NULL: even shares; else ascending within the input, with kBadRows in places
     bool listed;           // the call has a list of sequences (which may repeat itself)
 };
+constexpr int kBadRows = 1 << 30;   // in cu[i]: entry i is left out
 
 // The slots of a call are pages of its entries.  Without cu, entry i has `each`
 // of them; with cu, entry i's start at cu[i] / page_size + 2 i: n rows touch at
@@ -168,20 +169,16 @@ __device__ __forceinline__ Slot find_slot(const Kv8 &c, Lists l, long long slot,
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32;
             const int at = lo + lane * step;
-            const bool in = at < hi && (at == lo || (long long)(l.cu[at] >> c.page_shift) + 2LL * at <= slot);
+            const bool in = at < hi && (at == lo || (long long)((l.cu[at] & ~kBadRows) >> c.page_shift) + 2LL * at <= slot);
             const int k_in = 31 - __clz(__ballot_sync(0xffffffffu, in));   // lane 0 is always in
             hi = min(hi, lo + (k_in + 1) * step);
             lo = lo + k_in * step;
         }
         i = lo;
         row0 = l.cu[i];
-        const int end = l.cu[i + 1];
+        if (row0 & kBadRows) return out;   // (flagged with the list)
         j = slot - ((long long)(row0 >> c.page_shift) + 2LL * i);
-        if (row0 < 0 || end < row0 || end > tokens) {
-            if (teller && j == 0) kv8_flag(c, TP_MLP_KV8_BAD_LENGTH);
-            return out;
-        }
-        count = end - row0;
+        count = (l.cu[i + 1] & ~kBadRows) - row0;
     } else {
         i = (int)(slot / each);
         j = slot - (long long)i * each;
@@ -289,12 +286,43 @@ __device__ __forceinline__ void append_unit(const Kv8 &c, const T *k, const T *v
     }
 }
 
-__device__ __forceinline__ Lists take_lists(int *s_seq, int *s_cu, const int *seqs, const int *cu, int n) {
-    for (int x = threadIdx.x; x <= n; x += kThreads) {
-        if (x < n) s_seq[x] = kv8_seq(seqs, x);
-        if (cu) s_cu[x] = cu[x];
+// Brings a list of row bounds that is not ascending from 0 on within the input into that order (the search for a slot's
+// entry needs it), marks the entries whose own bounds are wrong (they begin before an earlier bound, or end before they
+// begin or behind the input), and flags them.  All threads of the block.
+__device__ __noinline__ void order_rows(const Kv8 &c, const int *s_seq, int *s_cu, bool listed, int n, int tokens) {
+    if (threadIdx.x == 0) {
+        int most = 0, at = s_cu[0];
+        for (int i = 0; i < n; ++i) {
+            const int next = s_cu[i + 1];
+            const bool ok = at >= most && next >= at && next <= tokens;
+            most = min(max(most, at), tokens);
+            s_cu[i] = ok ? most : most | kBadRows;
+            at = next;
+        }
+        s_cu[n] = min(max(most, at), tokens);
     }
     __syncthreads();
+    if (blockIdx.x != 0) return;
+    for (int i = threadIdx.x >> 5; i < n; i += kThreads / 32) {
+        const int seq = s_seq[i];
+        if (!(s_cu[i] & kBadRows) || seq == -1) continue;
+        const bool bad_seq = (unsigned)seq >= (unsigned)c.max_seqs || kv8_repeats(listed ? s_seq : nullptr, i, seq);
+        if ((threadIdx.x & 31) == 0) kv8_flag(c, bad_seq ? TP_MLP_KV8_BAD_SEQUENCE : TP_MLP_KV8_BAD_LENGTH);
+    }
+}
+
+__device__ __forceinline__ Lists take_lists(const Kv8 &c, int *s_seq, int *s_cu, const int *seqs, const int *cu, int n,
+                                            int tokens) {
+    bool off = false;
+    for (int x = threadIdx.x; x <= n; x += kThreads) {
+        if (x < n) s_seq[x] = kv8_seq(seqs, x);
+        if (cu) {
+            const int at = cu[x];
+            s_cu[x] = at;
+            off |= at < 0 || at > tokens || (x < n && cu[x + 1] < at);
+        }
+    }
+    if (__syncthreads_or(off)) order_rows(c, s_seq, s_cu, seqs != nullptr, n, tokens);
     return Lists{s_seq, cu ? s_cu : nullptr, seqs != nullptr};
 }
 
@@ -307,7 +335,7 @@ __global__ void __launch_bounds__(kThreads)
     pdl_allow_dependents();
     const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     pdl_wait_previous();
-    const Lists l = take_lists(s_seq, s_cu, seqs, cu, n);
+    const Lists l = take_lists(c, s_seq, s_cu, seqs, cu, n, tokens);
     if (unit >= units) return;
     const long long slot = unit / c.kv_heads;
     const int head = (int)(unit - slot * c.kv_heads);
@@ -329,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     const long long slot0 = u0 / c.kv_heads;
     const int head0 = (int)(u0 - slot0 * c.kv_heads);
     pdl_wait_previous();
-    const Lists l = take_lists(s_seq, s_cu, seqs, cu, n);
+    const Lists l = take_lists(c, s_seq, s_cu, seqs, cu, n, tokens);
     for (int x = threadIdx.x >> 5; x * c.kv_heads < head0 + run; x += kThreads / 32) {
         const bool teller = x > 0 || head0 == 0;   // the CTA that holds a slot's first unit sets its flags
         Slot sl = find_slot(c, l, slot0 + x, n, each, tokens, teller);

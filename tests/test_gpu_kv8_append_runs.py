@@ -107,3 +107,37 @@ def test_runs_as_long_as_a_cta_can_hold(dtype):
     assert int(cu[-1]) // 16 + 2 * n > 32 * resident(dtype)
     k, v = rows(r, int(cu[-1]), 1, 64, dtype)
     put(c, cache, 0, k, v, list(range(n)), cu)
+
+
+BOUNDS = [[-5, 3, 10, 30], [-40, -20, 12, 30], [0, 12, 5, 30], [0, 30, 10, 20], [4, 9, 20, 29], [0, 31, 31, 31], [-1, -1, -1, -1],
+          [0, 10, 2 ** 31 - 1, 30], [-2 ** 31, 10, 20, 30], [30, 20, 10, 0], [0, 20, 19, 20], [31, 40, 50, 60]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cu", BOUNDS)
+def test_row_bounds_out_of_order(cu, dtype):
+    """Each entry with wrong bounds is left out and flagged, wherever it stands; the others are written."""
+    r = np.random.default_rng(32)
+    c = filled(r, [33, 40, 37], 1, 3, 16, 64)
+    cache = on_gpu(c)
+    k, v = rows(r, 30, 3, 64, dtype)
+    put(c, cache, 0, k, v, [2, 0, 1], cu)
+    put(c, cache, 0, k, v, [-1, 1, 1], cu)                              # padded; one sequence twice
+    put(c, cache, 0, k, v, [7, 0, -2], cu)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_row_bounds_out_of_order_in_long_lists(dtype):
+    r = np.random.default_rng(33)
+    n = 500
+    new = [int(x) for x in r.integers(0, 60, n)]
+    c = filled(r, [0] * n, 1, 1, 16, 64, spare=5 * n, max_pages=5)
+    cache = on_gpu(c)
+    kv8.reserve(c, range(n), new)
+    cache.reserve(None, ints(new))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    k, v = rows(r, int(cu[-1]) + 3, 1, 64, dtype)                       # (rows of no entry behind the last)
+    for at, by in ((0, -70), (17, 1000), (40, -900), (333, 10 ** 7), (n, 4)):
+        off = cu.copy()
+        off[at] += by
+        put(c, cache, 0, k, v, list(range(n)), off)

@@ -240,3 +240,15 @@ def test_units_that_follow_each_other_use_two_buffers(tmp_path):
         assert [tuple(x) for x in got[:, :2]] == [x for x in units if bits >> x[0] & 1], (heads, head0, run, bits)
         assert (got[1:, 2] != got[:-1, 2]).all(), (heads, head0, run, bits)
         assert set(got[:, 2]) <= {0, 1}
+
+
+@pytest.mark.parametrize("cu,written", [([0, 4, 9, 12], [0, 1, 2]), ([-5, 3, 10, 12], [1, 2]), ([0, 8, 5, 12], [0]),
+                                        ([2, 4, 9, 10], [0, 1, 2]), ([0, 4, 13, 12], [0]), ([0, 12, 5, 9], [0])])
+def test_row_bounds_of_the_oracle(cu, written):
+    c = kv8.new_cache(1, 8, 1, 16, 64, 3, 2)
+    kv8.reserve(c, [0, 1, 2], [12, 12, 12])
+    c["k_scale"][:] = 7.0
+    x = np.ones((12, 1, 64))
+    want = kv8.BAD_LENGTH if len(written) < 3 else 0
+    assert kv8.append(c, 0, x, x, [0, 1, 2], cu) == want
+    assert [s for s in range(3) if c["k"][0, c["table"][s, 0], 0].any()] == written
