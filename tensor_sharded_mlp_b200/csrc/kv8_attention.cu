@@ -30,11 +30,15 @@
 // held in fp16, exactly for bf16 input (but for elements 2^-14 below the row's
 // largest, whose error is 2^-25 of it); fp32 input is held as two fp16 parts
 // (22 bits).  The running reference R is the maximum of s_t + log2(v_scale's
-// binade), in base-2 logs, so that the weight that multiplies the values,
-// w_t = 2^(s_t - R) v_scale, is at most 2^8 whatever the pages' scales; it is
-// rounded to fp16 for bf16 results (2^-11, under the result's 2^-8) and held as
-// two parts for fp32.  R moves only when a score exceeds it by 2^8 (one vote a
-// step; the sums are rescaled then).  Scores, sums and outputs are fp32.
+// binade), in base-2 logs, less 7, so that the largest weight that multiplies
+// the values, w_t = 2^(s_t - R) v_scale, lies between 2^6 and 2^15 whatever the
+// pages' scales.  It is rounded to fp16 for bf16 results (2^-11 of it, under the
+// result's 2^-8; below 2^-20 of the largest weight an absolute 2^-31 of that) and
+// held as two parts for fp32, the lower 2^12 times as large (2^-22 of it; 2^-43
+// of the largest).  R moves only when a score exceeds it by 2^15 (one vote a
+// step; the sums are rescaled then).  Scores, sums and outputs are fp32; the
+// mma's own sum, which cuts what it shifts out, carries bf16 outputs over a
+// warp's share (at most 2^-23 a step of 16 tokens, so 2^-11 at 64 Ki tokens).
 //
 // Warps whose pieces meet in one segment (entry, KV head, row tile) join them
 // in shared memory; pieces of a segment that CTAs share go to the workspace (at
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    m = fmaxf(ref[nt][x], m);
+                    m = fmaxf(ref[nt][x], m - kLift);
                     const float turn = m == ref[nt][x] ? 1.f : exp2_fast(ref[nt][x] - m);
                     ref[nt][x] = m;
                     sum[nt][x] *= turn;
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     w[y][0][nt][x] = transpose8x8(h);
                     if (kExact) {
                         const float2 b = widen_f16x2(h);
-                        w[y][kParts - 1][nt][x] = transpose8x8(f16x2(p[2 * x] - b.x, p[2 * x + 1] - b.y));
+                        w[y][kParts - 1][nt][x] = transpose8x8(f16x2((p[2 * x] - b.x) * kLow, (p[2 * x + 1] - b.y) * kLow));
                     }
                 }
             }
@@ -458,8 +462,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                             // the mma's own sum cuts what it shifts out: over thousands of steps that adds up, so for
                             // fp32 results a step's sum is added by an instruction that rounds
                             float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma(d, a0, a1, a2, a3, w[y][0][nt][0], w[y][0][nt][1]);
                             mma(d, a0, a1, a2, a3, w[y][kParts - 1][nt][0], w[y][kParts - 1][nt][1]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) d[k] *= 1.f / kLow;
+                            mma(d, a0, a1, a2, a3, w[y][0][nt][0], w[y][0][nt][1]);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) o[nt][2 * i + h][k] += d[k];
                         }

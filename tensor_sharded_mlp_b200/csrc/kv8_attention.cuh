@@ -15,8 +15,13 @@ namespace tpmlp {
 namespace {
 
 constexpr int kStep = 16;            // tokens of one step
-constexpr float kSlack = 8.f;        // how far (base-2 logs) a score may exceed the reference
-constexpr int kLeastLog = -88;       // smallest binade of a value scale in R: 2^31 weights of 2^(8 + 88) have a finite sum
+// A row's reference is set kLift (base-2 logs) below its largest s_t + log2(v_scale's binade), and stays until one exceeds
+// it by kSlack.  So the weights that multiply values reach from 2^6 .. 2^15, in the upper range of fp16, and have its full
+// precision down to 2^-14; one that is 2^-31 of the largest still counts (2^-25 is half of fp16's smallest number).
+constexpr float kLift = 7.f, kSlack = 15.f;
+constexpr int kLeastLog = -81;       // smallest binade of a value scale in R: 2^31 weights of 2^(15 + 81) have a finite sum
+// fp32 results: what fp16 cuts off a weight is held this much larger, in fp16 too (at most 2^3 * 2^12 there).
+constexpr float kLow = 4096.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxList = TP_MLP_KV8_MAX_LIST;
 constexpr int kWideRows = 128;         // query rows of a tile of the kernel for many rows

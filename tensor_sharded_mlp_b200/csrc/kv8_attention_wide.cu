@@ -12,7 +12,7 @@
 //   in the swizzled layout of the operands: keys K-major, values MN-major, so neither is transposed.
 // * Four warps do the softmax, a thread a row: it reads its scores from TMEM and writes its weights (fp16; the value
 //   scale and the reference R as in kv8_attention.cu) back to TMEM as the second product's A operand.  A tile is worked
-//   through once against the reference so far; only if a score exceeds that by 2^8 the reference moves, the outputs in
+//   through once against the reference so far; only if a score exceeds that by 2^15 the reference moves, the outputs in
 //   TMEM are rescaled and the tile is done again.
 // * One thread issues the products: the next tile's scores before this tile's outputs.
 // A value that is NaN would reach every row through 0 * NaN: the loaders take it out and mark the tile, and each row's
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
                             for (int k = 1; k < 16; ++k) x = fmaxf(x, s[k]);
                             m = fmaxf(m, x + vlog);
                         }
-                        ref = fmaxf(ref, m);
+                        ref = fmaxf(ref, m - kLift);
                     }
                     float part;
                     auto weights = [&]() {
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
                     };
                     weights();
                     if (__any_sync(0xffffffffu, m > ref + kSlack)) {
-                        const float up = fmaxf(ref, m), turn = up == ref ? 1.f : exp2_fast(ref - up);
+                        const float up = fmaxf(ref, m - kLift), turn = up == ref ? 1.f : exp2_fast(ref - up);
                         ref = up;
                         sum *= turn;
                         if (w.t > w.t0) {
