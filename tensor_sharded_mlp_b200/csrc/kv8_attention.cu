@@ -26,19 +26,20 @@
 // * The scales are constant over a step (a step lies in one page): the key
 //   scale multiplies the scores, the value scale the weights.
 //
-// Precision.  Queries are brought to [1, 2) by a power of two per row and
-// held in fp16, exactly for bf16 input (but for elements 2^-14 below the row's
-// largest, whose error is 2^-25 of it); fp32 input is held as two fp16 parts
-// (22 bits).  The running reference R is the maximum of s_t + log2(v_scale's
-// binade), in base-2 logs, less 7, so that the largest weight that multiplies
-// the values, w_t = 2^(s_t - R) v_scale, lies between 2^6 and 2^15 whatever the
-// pages' scales.  It is rounded to fp16 for bf16 results (2^-11 of it, under the
-// result's 2^-8; below 2^-20 of the largest weight an absolute 2^-31 of that) and
-// held as two parts for fp32, the lower 2^12 times as large (2^-22 of it; 2^-43
-// of the largest).  R moves only when a score exceeds it by 2^15 (one vote a
-// step; the sums are rescaled then).  Scores, sums and outputs are fp32; the
-// mma's own sum, which cuts what it shifts out, carries bf16 outputs over a
-// warp's share (at most 2^-23 a step of 16 tokens, so 2^-11 at 64 Ki tokens).
+// Precision.  Queries are brought to [2^14, 2^15) by a power of two per row and
+// held in fp16, exactly for bf16 input (but for elements 2^-31 below the row's
+// largest, whose error is 2^-39 of it); fp32 input is held as two fp16 parts
+// (22 bits of an element, 2^-39 of the largest at worst).  The running reference
+// R is the maximum of s_t + log2(v_scale's binade), in base-2 logs, less 7, so
+// that the largest weight that multiplies the values, w_t = 2^(s_t - R) v_scale,
+// lies between 2^6 and 2^15 whatever the pages' scales.  It is rounded to fp16
+// for bf16 results (2^-11 of it, under the result's 2^-8; below 2^-20 of the
+// largest weight an absolute 2^-31 of that) and held as two parts for fp32, the
+// lower 2^12 times as large (2^-22 of it; 2^-43 of the largest).  R moves only
+// when a score exceeds it by 2^15 (one vote a step; the sums are rescaled then).
+// Scores, sums and outputs are fp32; the mma's own sum, which cuts what it
+// shifts out, carries bf16 outputs over a warp's share (at most 2^-23 a step of
+// 16 tokens, so 2^-11 at 64 Ki tokens).
 //
 // Warps whose pieces meet in one segment (entry, KV head, row tile) join them
 // in shared memory; pieces of a segment that CTAs share go to the workspace (at

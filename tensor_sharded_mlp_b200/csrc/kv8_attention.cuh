@@ -151,14 +151,15 @@ template <> struct RawQuery<float> {
     }
 };
 
-// A query row is brought to [1, 2) by a power of two (`down`), which the scores get back (`up`).
+// A query row is brought to [2^14, 2^15) by a power of two (`down`), which the scores get back (`up`): the upper end of
+// fp16, so that elements far below the row's largest (which may meet keys near zero) keep their bits too.  Rows below
+// 2^-112 are brought up by 2^126 only, the largest power of two that has an inverse among normal numbers.
 struct QueryScale {
     float down, up;
 };
 __device__ __forceinline__ QueryScale query_scale(float amax) {
-    const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 127);
+    const int ex = max((int)(__float_as_uint(amax) >> 23) - 127, -112) - 14;   // -126 .. 113
     const float down = amax > FLT_MAX ? NAN   // an infinity in a row makes its scores, and so its result, NaN
-                       : ex == 127    ? 0x1p-127f
                                       : __uint_as_float((uint32_t)(127 - ex) << 23);   // 2^-ex
     return {down, __uint_as_float((uint32_t)(ex + 127) << 23)};
 }

@@ -10,8 +10,9 @@ import numpy as np
 import pytest
 import torch
 
-from kv8_helpers import HALF, close, flags, ints, on_gpu, score_bound, weight_bound
+from kv8_helpers import HALF, close, filled, flags, ints, on_gpu, score_bound, weight_bound
 from oracle import kv8
+from test_gpu_kv8_attention import check, query
 
 pytestmark = pytest.mark.gpu
 TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -114,3 +115,17 @@ def test_scores_within_the_slack_of_the_reference(dtype, head_dim, q_len, heads)
     h = History([key], [value], head_dim, page=32, v_scale=float(np.float32(1.99)))
     for top in (4.5, 5.5, 6.5, 7.5, 7.9, 8.5, 14.5, 15.5):              # base-2 logs above the first tokens
         h.check(1.0, q_len, heads, dtype, float(np.float32(top / 15.0 * np.log(2.0))), f"2^{top}")
+
+
+@pytest.mark.parametrize("dtype,head_dim,q_len,heads,size", [(*x, 2.0 ** (13 if x[0] == "f32" else 20)) for x in SHAPES] +
+                         [("f32", 128, 1, 8, 2.0 ** 16), ("bf16", 128, 1, 8, 2.0 ** 22), ("bf16", 128, 9, 8, 2.0 ** 22)])
+def test_a_query_element_far_above_the_others(dtype, head_dim, q_len, heads, size):
+    """It meets keys of zero, so the scores are the other elements' alone, within the bound of their own products."""
+    r = np.random.default_rng(head_dim + heads)
+    c = filled(r, [300, 45], 1, 1, 32, head_dim)
+    for s in range(2):
+        for t in range(int(c["lengths"][s])):
+            c["k"][0, c["table"][s, t // 32], 0, t % 32, 3] = 0
+    q = query(r, 2, q_len, heads, head_dim, dtype)
+    q[..., 3] = size
+    check(c, on_gpu(c), q, [0, 1])
