@@ -707,6 +707,20 @@ int tp_mlp_kv8_attention_partials(const tp_mlp_kv8_cache *cache, int layer, cons
                                   int dtype, float *maximum, float *exp_sum, void *weighted, void *workspace,
                                   size_t workspace_bytes, tp_mlp_stream_t stream);
 
+/*
+ * Self-test of the bounded waits inside the attention kernel for many query
+ * rows: the call of tp_mlp_kv8_attention with scale 1, bf16 dense queries and
+ * sequences 0 .. n - 1, in which one of the kernel's roles (0: loads, 1: softmax
+ * weights, 2: products) delivers nothing from `tile` (>= 0) of each CTA on, and
+ * waits give up after wait_us microseconds (1..100000).  A CTA whose work
+ * reaches that tile ends with TP_MLP_KV8_TIMEOUT in the status word and its
+ * results not valid; nothing traps, and the context stays usable.  A call that
+ * the kernel for few rows would take is refused (TP_MLP_ERR_UNSUPPORTED).
+ */
+int tp_mlp_kv8_selftest_stalled_attention(const tp_mlp_kv8_cache *cache, int layer, const void *q, int n, int q_len,
+                                          int heads, void *out, void *workspace, size_t workspace_bytes, int role,
+                                          int tile, unsigned wait_us, tp_mlp_stream_t stream);
+
 /* Human-readable name of a status code (static string; no counterpart in the pages). */
 const char *tp_mlp_status_string(int status);
 

@@ -91,6 +91,7 @@ _SIGS = {
     "tp_mlp_kv8_append": (_i, [_kv8, _i, _vp, _vp, _ll, _i, _vp, _vp, _i, _i, _vp]),
     "tp_mlp_kv8_attention_workspace_bytes": (_sz, [_kv8, _i, _i, _i]),
     "tp_mlp_kv8_attention": (_i, [_kv8, _i, _vp, _ll, _vp, _vp, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _sz, _vp]),
+    "tp_mlp_kv8_selftest_stalled_attention": (_i, [_kv8, _i, _vp, _i, _i, _i, _vp, _vp, _sz, _i, _i, ctypes.c_uint, _vp]),
     "tp_mlp_kv8_attention_partials": (_i, [_kv8, _i, _vp, _ll, _vp, _vp, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _vp,
                                            _vp, _sz, _vp]),
 }
@@ -595,6 +596,17 @@ def tp_mlp_kv8_attention_partials(cache: Kv8Cache, layer: int, q: torch.Tensor, 
                                               _ptr(weighted), _ptr(ws), ws.numel(),
                                               _stream(stream)))
     return maximum, exp_sum, weighted
+
+
+def tp_mlp_kv8_selftest_stalled_attention(cache: Kv8Cache, layer: int, q: torch.Tensor, out: torch.Tensor, role: int,
+                                          tile: int, wait_us: int, stream=None) -> None:
+    """The many-rows attention with a role (0 loads, 1 weights, 2 products) that stops at a tile, and short waits."""
+    n, q_len, heads, _ = _kv8_query(cache, _dense(q, q.shape, torch.bfloat16, "q"), None, None)
+    _dense(out, q.shape, q.dtype, "out")
+    ws = _kv8_workspace(cache, q_len, heads, stream)
+    _check("tp_mlp_kv8_selftest_stalled_attention",
+           _lib.tp_mlp_kv8_selftest_stalled_attention(cache, layer, _ptr(q), n, q_len, heads, _ptr(out), _ptr(ws),
+                                                      ws.numel(), role, tile, wait_us, _stream(stream)))
 
 
 # --- convenience wrapper -----------------------------------------------------------

@@ -56,6 +56,13 @@ __device__ __forceinline__ float4 e4m3_unpack4(uint32_t w) {
 cudaError_t launch_kv8_append(const Kv8 &c, const void *k, const void *v, long long row_stride, int tokens,
                               const int *seqs, const int *cu, int n, int dtype, int num_sms, cudaStream_t st);
 
+// For the test of the bounded waits: from which tile of a CTA on a role of the many-rows kernel delivers nothing, and
+// after how long waits give up (0: an ordinary call).
+struct Kv8Stall {
+    int loads = 0x7fffffff, weights = 0x7fffffff, products = 0x7fffffff;
+    unsigned wait_us = 0;
+};
+
 // kv8_attention.cu.  maximum != nullptr: the partial form (o = weighted).
 struct Kv8Query {
     const void *q;
@@ -66,6 +73,7 @@ struct Kv8Query {
     int dtype;
     void *o;
     float *maximum, *exp_sum;
+    Kv8Stall stall;
 };
 // kv8_attention_wide.cu: the form for many query rows a KV head
 bool kv8_wide_rows(const Kv8 &c, int q_len, int heads);            // whether they are

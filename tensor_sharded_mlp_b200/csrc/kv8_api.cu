@@ -262,7 +262,7 @@ size_t tp_mlp_kv8_attention_workspace_bytes(const tp_mlp_kv8_cache *cache, int n
 int tp_mlp_kv8_attention(const tp_mlp_kv8_cache *cache, int layer, const void *q, long long row_stride,
                          const int *seqs, const int *positions, int n, int q_len, int heads, float scale, int dtype,
                          void *out, void *workspace, size_t workspace_bytes, tp_mlp_stream_t stream) {
-    const Kv8Query a = {q, row_stride, seqs, positions, n, q_len, heads, scale, dtype, out, nullptr, nullptr};
+    const Kv8Query a = {q, row_stride, seqs, positions, n, q_len, heads, scale, dtype, out, nullptr, nullptr, {}};
     return attention(cache, layer, a, false, workspace, workspace_bytes, stream);
 }
 
@@ -270,8 +270,24 @@ int tp_mlp_kv8_attention_partials(const tp_mlp_kv8_cache *cache, int layer, cons
                                   const int *seqs, const int *positions, int n, int q_len, int heads, float scale,
                                   int dtype, float *maximum, float *exp_sum, void *weighted, void *workspace,
                                   size_t workspace_bytes, tp_mlp_stream_t stream) {
-    const Kv8Query a = {q, row_stride, seqs, positions, n, q_len, heads, scale, dtype, weighted, maximum, exp_sum};
+    const Kv8Query a = {q, row_stride, seqs, positions, n, q_len, heads, scale, dtype, weighted, maximum, exp_sum, {}};
     return attention(cache, layer, a, true, workspace, workspace_bytes, stream);
+}
+
+int tp_mlp_kv8_selftest_stalled_attention(const tp_mlp_kv8_cache *cache, int layer, const void *q, int n, int q_len,
+                                          int heads, void *out, void *workspace, size_t workspace_bytes, int role,
+                                          int tile, unsigned wait_us, tp_mlp_stream_t stream) {
+    Kv8 c;
+    const int s = view_of(cache, &c);
+    if (s) return s;
+    if (attention_sizes(c, n, q_len, heads)) return TP_MLP_ERR_SHAPE;
+    if (role < 0 || role > 2 || tile < 0 || wait_us == 0 || wait_us > 100000) return TP_MLP_ERR_INVALID_ARG;
+    if (!kv8_wide_rows(c, q_len, heads)) return TP_MLP_ERR_UNSUPPORTED;
+    Kv8Query a = {q, (long long)heads * c.head_dim, nullptr, nullptr, n, q_len, heads, 1.f, TP_MLP_BF16, out, nullptr,
+                  nullptr, {}};
+    (role == 0 ? a.stall.loads : role == 1 ? a.stall.weights : a.stall.products) = tile;
+    a.stall.wait_us = wait_us;
+    return attention(cache, layer, a, false, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -94,7 +94,8 @@ struct Walk {
     bool live;
 };
 
-template <int D>
+// kStalls: the form for the test of the waits, in which a role stops (Kv8Stall).
+template <int D, bool kStalls>
 __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
     attention_wide_kernel(Kv8 c, Kv8Query a, Split ws, int row_tiles) {
     using C = WideCfg<D>;
@@ -188,7 +189,9 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_base;
-    auto wait = [&](uint32_t bar, int phase) { return tc::mbar_wait(bar, phase & 1, &gave_up); };
+    auto wait = [&](uint32_t bar, int phase) {
+        return tc::mbar_wait(bar, phase & 1, &gave_up, kStalls ? a.stall.wait_us * 1000ull : tc::kWaitLimitNs);
+    };
 
     if (warp >= 4 && warp < 12) {
         // --- loads: codes of two tiles in registers, the pages of the tile behind them ----------------------------
@@ -238,6 +241,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
         auto store = [&](Raw &r, int i) {
             const int slot = i & 1;
             if (i >= 2 && !__all_sync(0xffffffffu, wait(kv_empty + 8 * slot, (i >> 1) - 1))) return false;
+            if (kStalls && i >= a.stall.loads) return false;
             uint32_t any = 0;
 #pragma unroll
             for (int x = 0; x < kChunks; ++x)
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
                 }
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(p_full + 8 * slot);
+                if (lane == 0 && !(kStalls && i >= a.stall.weights)) tc::mbar_arrive(p_full + 8 * slot);
             }
             if (!ok || !(ok = outputs_done())) break;
             tc::tc_fence_after();
@@ -488,6 +492,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
             }
             next_segment();
         }
+        if (!ok) tmem_st_wait();   // (weights on their way when a wait gave up)
     } else if (lane == 0) {
         // --- products -------------------------------------------------------------------------------------------
         constexpr uint32_t kF16 = (1u << 4) | ((uint32_t)(kWideRows >> 4) << 24);      // f16 x f16 -> f32, M = 128
@@ -512,6 +517,7 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
         while (ok && w.live) {
             const bool first = w.t == w.t0;
             const int slot = i & 1;
+            if (kStalls && i >= a.stall.products) break;
             if (first) {       // (the row threads turn to the next segment once this one's outputs are there)
                 if (open) outputs();
                 if (!ok || !(ok = wait(q_full, seg))) break;
@@ -534,11 +540,10 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
             if (++w.t == w.t1) next_segment();
         }
         if (ok && open) outputs();
-        if (!ok) {             // products in flight end before the memory is given back
-            volatile int none = 0;
-            tc::mma_commit(done);
-            tc::mbar_wait(done, 0, &none);
-        }
+        // products in flight end before the memory is given back, whichever role's wait gave up
+        volatile int none = 0;
+        tc::mma_commit(done);
+        tc::mbar_wait(done, 0, &none);
     }
     __syncwarp();
     tc::tc_fence_before();
@@ -551,17 +556,22 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
     if (tid == 0 && gave_up) kv8_flag(c, TP_MLP_KV8_TIMEOUT);
 }
 
-template <int D>
+template <int D, bool kStalls>
 cudaError_t launch_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
     using C = WideCfg<D>;
     const int row_tiles = (a.q_len * (a.heads / c.kv_heads) + kWideRows - 1) / kWideRows;
     const Split s = split_of(ws, num_sms);
-    auto kern = attention_wide_kernel<D>;
+    auto kern = attention_wide_kernel<D, kStalls>;
     cudaError_t e = ensure_smem_attr(kern, C::smem(kMaxList));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)num_sms), dim3(C::kThreads), C::smem(a.n), st, c, a, s, row_tiles);
     if (e != cudaSuccess) return e;
     return launch_combine<__nv_bfloat16, D, kWideRows>(c, a, s, row_tiles, num_sms, st);
+}
+
+template <int D>
+cudaError_t launch_either(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
+    return a.stall.wait_us ? launch_wide<D, true>(c, a, ws, num_sms, st) : launch_wide<D, false>(c, a, ws, num_sms, st);
 }
 
 }  // namespace
@@ -575,9 +585,9 @@ bool kv8_wide_rows(const Kv8 &c, int q_len, int heads) {
 }
 
 cudaError_t launch_kv8_attention_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
-    if (c.head_dim == 64) return launch_wide<64>(c, a, ws, num_sms, st);
-    if (c.head_dim == 128) return launch_wide<128>(c, a, ws, num_sms, st);
-    return launch_wide<256>(c, a, ws, num_sms, st);
+    if (c.head_dim == 64) return launch_either<64>(c, a, ws, num_sms, st);
+    if (c.head_dim == 128) return launch_either<128>(c, a, ws, num_sms, st);
+    return launch_either<256>(c, a, ws, num_sms, st);
 }
 
 }  // namespace tpmlp

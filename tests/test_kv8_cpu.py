@@ -252,3 +252,16 @@ def test_row_bounds_of_the_oracle(cu, written):
     want = kv8.BAD_LENGTH if len(written) < 3 else 0
     assert kv8.append(c, 0, x, x, [0, 1, 2], cu) == want
     assert [s for s in range(3) if c["k"][0, c["table"][s, 0], 0].any()] == written
+
+
+def test_stalled_attention_is_refused(b):
+    L, p, ws = b._lib.tp_mlp_kv8_selftest_stalled_attention, ctypes.c_void_p(0x100000), 1 << 30
+    c = _cache(b)
+    assert L(None, 0, p, 1, 100, 2, p, p, ws, 0, 0, 10, None) == 1
+    assert L(_cache(b, page_size=24), 0, p, 1, 100, 2, p, p, ws, 0, 0, 10, None) == 2
+    assert L(c, 0, p, 1, 129, 2, p, p, ws, 0, 0, 10, None) == 2
+    for role, tile, wait in ((-1, 0, 10), (3, 0, 10), (0, -1, 10), (0, 0, 0), (0, 0, 100001)):
+        assert L(c, 0, p, 1, 100, 2, p, p, ws, role, tile, wait, None) == 1
+    assert L(c, 0, p, 1, 16, 2, p, p, ws, 0, 0, 10, None) == 4            # few rows
+    assert L(c, 2, p, 1, 100, 2, p, p, ws, 0, 0, 10, None) == 2           # layer
+    assert L(c, 0, None, 1, 100, 2, p, p, ws, 0, 0, 10, None) == 1
