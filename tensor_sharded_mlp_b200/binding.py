@@ -547,9 +547,11 @@ def _kv8_query(cache: Kv8Cache, q: torch.Tensor, seqs, positions):
 
 def _kv8_workspace(cache: Kv8Cache, q_len: int, heads: int, stream) -> torch.Tensor:
     # (it holds pieces of rows for each SM: the same for any n and any history)
-    if cache.attention_workspace[:2] != (q_len, heads):
-        cache.attention_workspace = (q_len, heads, int(_lib.tp_mlp_kv8_attention_workspace_bytes(cache, 1, q_len, heads)))
-    return _scratch(cache.attention_workspace[2], stream)
+    last = cache.attention_workspace     # (looked at once: another thread's call may put its own there)
+    if last[:2] != (q_len, heads):
+        last = (q_len, heads, int(_lib.tp_mlp_kv8_attention_workspace_bytes(cache, 1, q_len, heads)))
+        cache.attention_workspace = last
+    return _scratch(last[2], stream)
 
 
 def _dense(t: torch.Tensor, shape, dtype, what: str) -> torch.Tensor:

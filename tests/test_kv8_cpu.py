@@ -265,3 +265,24 @@ def test_stalled_attention_is_refused(b):
     assert L(c, 0, p, 1, 16, 2, p, p, ws, 0, 0, 10, None) == 4            # few rows
     assert L(c, 2, p, 1, 100, 2, p, p, ws, 0, 0, 10, None) == 2           # layer
     assert L(c, 0, None, 1, 100, 2, p, p, ws, 0, 0, 10, None) == 1
+
+
+def test_calls_of_two_threads_get_their_own_workspace(b, monkeypatch):
+    """Another thread's call between two looks at the size kept on the cache must not change this call's scratch."""
+    class Shared(b.Kv8Cache):
+        looks = 0
+
+        @property
+        def attention_workspace(self):
+            Shared.looks += 1
+            return (128, 2, 1 << 20) if Shared.looks == 1 else (1, 2, 16)   # from the second look on the other thread's
+
+        @attention_workspace.setter
+        def attention_workspace(self, value):
+            pass
+
+    monkeypatch.setattr(b, "_scratch", lambda nbytes, stream: nbytes)
+    c = Shared.from_buffer_copy(_cache(b))
+    assert b._kv8_workspace(c, 128, 2, None) == 1 << 20
+    Shared.looks = 1                                                      # not kept: asked for, and not looked up again
+    assert b._kv8_workspace(c, 128, 2, None) == b._lib.tp_mlp_kv8_attention_workspace_bytes(c, 1, 128, 2)
