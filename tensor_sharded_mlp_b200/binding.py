@@ -129,7 +129,12 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:   # the current stream's handle, without building a Stream object (0.2 us against 3.5)
         return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(_current_device()))
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return ctypes.c_void_p(_handle(stream))
+
+
+def _handle(stream) -> int:
+    """A stream object's (torch's or another library's) or a plain handle's number."""
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr_array(ts: Sequence[torch.Tensor], n: int):
@@ -439,7 +444,7 @@ def _scratch(nbytes: int, stream) -> torch.Tensor:
 def _made_for(t: torch.Tensor, stream) -> torch.Tensor:
     """A tensor allocated on the current stream for a call on `stream` (None: the same)."""
     if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream)))
     return t
 
 
