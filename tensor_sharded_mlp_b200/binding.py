@@ -435,16 +435,30 @@ def _here(t: torch.Tensor) -> bool:
     return t.is_cuda and t.get_device() == _current_device()
 
 
+def _on(stream):
+    """Context in which torch allocates on the call's stream.  Memory from the
+    current stream's pool may still be in use by work queued there, which a call
+    on another stream does not wait for."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream)))
+
+
 def _scratch(nbytes: int, stream) -> torch.Tensor:
     """Device scratch for one call: torch hands the memory out again only to
     work behind the call (under capture it belongs to the graph)."""
-    return _made_for(torch.empty(nbytes, dtype=torch.uint8, device="cuda"), stream)
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    with _on(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
-def _made_for(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor allocated on the current stream for a call on `stream` (None: the same)."""
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream)))
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A call's result, allocated on the call's stream and marked as used on the
+    current one, so that its memory is kept until both are done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 
@@ -570,8 +584,7 @@ def tp_mlp_kv8_attention(cache: Kv8Cache, layer: int, q: torch.Tensor, scale: fl
                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of q (n, q_len, heads, head_dim) over one layer of the cache."""
     n, q_len, heads, stride = _kv8_query(cache, q, seqs, positions)
-    out = _made_for(torch.empty_like(q, memory_format=torch.contiguous_format), stream) if out is None else \
-        _dense(out, q.shape, q.dtype, "out")
+    out = _new(q.shape, q.dtype, q.device, stream) if out is None else _dense(out, q.shape, q.dtype, "out")
     ws = _kv8_workspace(cache, q_len, heads, stream)
     _check("tp_mlp_kv8_attention",
            _lib.tp_mlp_kv8_attention(cache, layer, _ptr(q), stride, _ptr(seqs), _ptr(positions), n, q_len, heads,
@@ -590,11 +603,11 @@ def tp_mlp_kv8_attention_partials(cache: Kv8Cache, layer: int, q: torch.Tensor, 
 
     def stat(t, what):
         if t is None:
-            return _made_for(torch.empty(n, q_len, heads, dtype=torch.float32, device=q.device), stream)
+            return _new((n, q_len, heads), torch.float32, q.device, stream)
         return _dense(t, (n, q_len, heads), torch.float32, what)
 
     maximum, exp_sum = stat(maximum, "maximum"), stat(exp_sum, "exp_sum")
-    weighted = _made_for(torch.empty_like(q, memory_format=torch.contiguous_format), stream) if weighted is None else \
+    weighted = _new(q.shape, q.dtype, q.device, stream) if weighted is None else \
         _dense(weighted, q.shape, q.dtype, "weighted")
     ws = _kv8_workspace(cache, q_len, heads, stream)
     _check("tp_mlp_kv8_attention_partials",
