@@ -286,3 +286,18 @@ def test_calls_of_two_threads_get_their_own_workspace(b, monkeypatch):
     assert b._kv8_workspace(c, 128, 2, None) == 1 << 20
     Shared.looks = 1                                                      # not kept: asked for, and not looked up again
     assert b._kv8_workspace(c, 128, 2, None) == b._lib.tp_mlp_kv8_attention_workspace_bytes(c, 1, 128, 2)
+
+
+def test_a_torch_without_the_private_functions(b, monkeypatch):
+    """The current device and stream come from torch's public calls then, for every wrapper."""
+    class Stream:
+        cuda_stream = 0x1234
+
+    for name in ("_get_device", "_get_stream"):
+        monkeypatch.setattr(b, name, None)
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream())
+    assert b._current_device() == 3
+    assert b._stream(None).value == 0x1234 and b._stream(Stream()).value == 0x1234 and b._stream(0x99).value == 0x99
