@@ -609,7 +609,8 @@ int tp_mlp_kv8_reserve(const tp_mlp_kv8_cache *cache, const int *seqs, const int
  * go up, no contents move; tp_mlp_kv8_reserve copies a shared page when it is
  * written to).  A child must be empty (length 0), may be in the list once, and
  * may not be a parent in the same list; a pair that breaks this is left out
- * and flagged.  Both lists: device, n ints, n <= TP_MLP_KV8_MAX_LIST.
+ * and flagged.  A pair with a -1 is unused, and its other number counts for
+ * nothing.  Both lists: device, n ints, n <= TP_MLP_KV8_MAX_LIST.
  */
 int tp_mlp_kv8_fork(const tp_mlp_kv8_cache *cache, const int *parents, const int *children, int n,
                     tp_mlp_stream_t stream);

@@ -126,11 +126,11 @@ def reserve(c, seqs, counts):
 def fork(c, parents, children):
     flags, seen, pairs = 0, set(), []
     seqs = len(c["lengths"])
+    used = {int(p) for p, s in zip(parents, children) if p != -1 and s != -1}
     for p, s in zip(parents, children):
         if p == -1 or s == -1:
-            seen.add(int(s))
             continue
-        if not (0 <= p < seqs and 0 <= s < seqs) or s in seen or s in parents:
+        if not (0 <= p < seqs and 0 <= s < seqs) or s in seen or s in used:
             flags |= BAD_SEQUENCE
         else:
             pairs.append((int(p), int(s)))

@@ -343,14 +343,15 @@ __global__ void __launch_bounds__(kRowThreads)
     pdl_wait_previous();
     const int parent = parents[i], child = children[i];
     if (parent == -1 || child == -1) return;
-    int bad = 0;
-    if ((unsigned)parent >= (unsigned)c.max_seqs || (unsigned)child >= (unsigned)c.max_seqs)
-        bad = TP_MLP_KV8_BAD_SEQUENCE;
-    // no child is read as a parent by any CTA, so no CTA sees another's writes
-    else if (block_finds(children, i, child) | block_finds(parents, n, child))
-        bad = TP_MLP_KV8_BAD_SEQUENCE;
-    if (bad) {
-        if (threadIdx.x == 0) kv8_flag(c, bad);
+    bool bad = (unsigned)parent >= (unsigned)c.max_seqs || (unsigned)child >= (unsigned)c.max_seqs;
+    if (!bad) {   // a child before, or a parent, in a pair that is in use: no CTA sees another's writes
+        for (int j = threadIdx.x; j < n; j += kRowThreads) {
+            const int p = parents[j], s = children[j];
+            bad |= p != -1 && s != -1 && (p == child || (j < i && s == child));
+        }
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) kv8_flag(c, TP_MLP_KV8_BAD_SEQUENCE);
         return;
     }
     const int len = c.lengths[parent], was = c.lengths[child];

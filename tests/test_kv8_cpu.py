@@ -301,3 +301,13 @@ def test_a_torch_without_the_private_functions(b, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream())
     assert b._current_device() == 3
     assert b._stream(None).value == 0x1234 and b._stream(Stream()).value == 0x1234 and b._stream(0x99).value == 0x99
+
+
+@pytest.mark.parametrize("parents,children,made,flags", [([-1, 0], [2, 2], [2], 0), ([3, 0], [-1, 3], [3], 0),
+                                                         ([-1, 0, 0], [2, 2, 2], [2], kv8.BAD_SEQUENCE),
+                                                         ([0, 2], [2, 3], [], kv8.BAD_SEQUENCE)])
+def test_unused_pairs_of_the_oracles_fork(parents, children, made, flags):
+    c = kv8.new_cache(1, 4, 1, 16, 64, 4, 2)
+    kv8.reserve(c, [0], [20])
+    assert kv8.fork(c, parents, children) == flags
+    assert [s for s in (2, 3) if c["lengths"][s]] == made
