@@ -76,7 +76,8 @@ struct Kv8Query {
     Kv8Stall stall;
 };
 // kv8_attention_wide.cu: the form for many query rows a KV head
-bool kv8_wide_rows(const Kv8 &c, int q_len, int heads);            // whether they are
+bool kv8_wide_rows(const Kv8 &c, int n, int q_len, int heads);     // whether a call takes it
+bool kv8_may_be_wide(const Kv8 &c, int q_len, int heads);          // whether a call of any number of entries does
 cudaError_t launch_kv8_attention_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st);
 size_t kv8_attention_workspace(const Kv8 &c, int q_len, int heads, int num_sms);
 cudaError_t launch_kv8_attention(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st);

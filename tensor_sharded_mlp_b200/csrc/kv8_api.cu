@@ -282,7 +282,7 @@ int tp_mlp_kv8_selftest_stalled_attention(const tp_mlp_kv8_cache *cache, int lay
     if (s) return s;
     if (attention_sizes(c, n, q_len, heads)) return TP_MLP_ERR_SHAPE;
     if (role < 0 || role > 2 || tile < 0 || wait_us == 0 || wait_us > 100000) return TP_MLP_ERR_INVALID_ARG;
-    if (!kv8_wide_rows(c, q_len, heads)) return TP_MLP_ERR_UNSUPPORTED;
+    if (!kv8_wide_rows(c, n, q_len, heads)) return TP_MLP_ERR_UNSUPPORTED;
     Kv8Query a = {q, (long long)heads * c.head_dim, nullptr, nullptr, n, q_len, heads, 1.f, TP_MLP_BF16, out, nullptr,
                   nullptr, {}};
     (role == 0 ? a.stall.loads : role == 1 ? a.stall.weights : a.stall.products) = tile;

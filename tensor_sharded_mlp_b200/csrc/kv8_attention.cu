@@ -784,13 +784,13 @@ cudaError_t launch_typed(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms,
 // Two pieces per CTA of the widest row tile.
 size_t kv8_attention_workspace(const Kv8 &c, int q_len, int heads, int num_sms) {
     int rows = 8 * (c.head_dim == 64 ? wide_tiles<64>() : c.head_dim == 128 ? wide_tiles<128>() : wide_tiles<256>());
-    if (kv8_wide_rows(c, q_len, heads)) rows = kWideRows;
+    if (kv8_may_be_wide(c, q_len, heads)) rows = kWideRows;
     return align256((size_t)num_sms * sizeof(int4)) + align256((size_t)num_sms * 2 * rows * (c.head_dim + 4) * sizeof(float));
 }
 
 cudaError_t launch_kv8_attention(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
     if (a.dtype == TP_MLP_F32) return launch_typed<float>(c, a, ws, num_sms, st);
-    if (kv8_wide_rows(c, a.q_len, a.heads)) return launch_kv8_attention_wide(c, a, ws, num_sms, st);
+    if (kv8_wide_rows(c, a.n, a.q_len, a.heads)) return launch_kv8_attention_wide(c, a, ws, num_sms, st);
     return launch_typed<__nv_bfloat16>(c, a, ws, num_sms, st);
 }
 

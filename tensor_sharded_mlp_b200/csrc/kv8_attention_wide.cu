@@ -576,12 +576,31 @@ cudaError_t launch_either(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms
 
 }  // namespace
 
-// From where on the products bound the other kernel.  At 64 rows a long history gains here (head_dim 64 / 128 / 256: 75 -> 78,
-// 118 -> 90, 292 -> 154 us) and a short one loses: a segment's queries, outputs and join cost more (one sequence of 4000
-// tokens: 72 rows 22 -> 22, 20 -> 25, 38 -> 40 us; 128 rows 24 -> 25, 25 -> 28, 45 -> 48; 8 of 100 to 300 tokens, 128 rows:
-// 21 -> 18, 20 -> 22, 29 -> 43).
-bool kv8_wide_rows(const Kv8 &c, int q_len, int heads) {
-    return q_len * (heads / c.kv_heads) > 64;
+// From so many rows on the products bound the other kernel, whose row tiles (32, 16 or 8 rows for head_dim 64, 128, 256)
+// each read the history again; but it cuts a short history finer, and a segment's queries, outputs and join cost less there.
+// Both in us, 8 KV heads, other kernel / this one:
+//                                 16 x 4000 tokens  32 x 1000    64 x 200     8 x 100-300  1 x 4000
+//   head_dim 256, 24 rows           107 / 147         61 / 105     37 / 100    15 / 25      19 / 35
+//                 33                195 / 148         93 / 108     51 / 103    16 / 26      23 / 38
+//                 64                288 / 150        144 / 110     77 / 107    19 / 28      28 / 38
+//   head_dim 128, 48 rows            92 / 90          55 / 64      36 / 58     15 / 18      17 / 23
+//                 64                119 / 91          69 / 65      44 / 58     16 / 18      18 / 24
+//   head_dim 64,  33-64 rows         76 / 73-74       49-50 / 50   38 / 43     18 / 15      22 / 21
+// The lengths are the device's to know.  The host has a bound of the tokens that a call can see, and up to 64 rows this
+// kernel is taken only where those of all KV heads may be 2^18 (16 x 4000 x 8 are 2^19, 32 x 1000 x 8 are 2^18).
+namespace {
+constexpr int kAlwaysWide = 64;
+int wide_rows_from(int head_dim) { return head_dim == 256 ? 32 : head_dim == 128 ? 48 : kAlwaysWide; }
+}  // namespace
+
+bool kv8_may_be_wide(const Kv8 &c, int q_len, int heads) {
+    return q_len * (heads / c.kv_heads) > wide_rows_from(c.head_dim);
+}
+
+bool kv8_wide_rows(const Kv8 &c, int n, int q_len, int heads) {
+    const long long pages = (long long)n * c.max_pages < c.num_pages ? (long long)n * c.max_pages : c.num_pages;
+    return kv8_may_be_wide(c, q_len, heads) &&
+           (q_len * (heads / c.kv_heads) > kAlwaysWide || pages * c.page_size * c.kv_heads >= 1LL << 18);
 }
 
 cudaError_t launch_kv8_attention_wide(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms, cudaStream_t st) {
