@@ -460,15 +460,22 @@ def _scratch(nbytes: int, stream) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
+def _new(stream, *shape: int, dtype, device) -> torch.Tensor:
     """A call's result, allocated on the call's stream and marked as used on the
     current one, so that its memory is kept until both are done with it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with _on(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(*shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream())
     return t
+
+
+def _new_like(stream, t: torch.Tensor) -> torch.Tensor:
+    """The same, with a tensor's shape and type (the quickest way to allocate it)."""
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _new(stream, *t.shape, dtype=t.dtype, device=t.device)
 
 
 def _rows(t: torch.Tensor, what: str, dims: int, heads: int, head_dim: int) -> int:
@@ -593,7 +600,7 @@ def tp_mlp_kv8_attention(cache: Kv8Cache, layer: int, q: torch.Tensor, scale: fl
                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of q (n, q_len, heads, head_dim) over one layer of the cache."""
     n, q_len, heads, stride = _kv8_query(cache, q, seqs, positions)
-    out = _new(q.shape, q.dtype, q.device, stream) if out is None else _dense(out, q.shape, q.dtype, "out")
+    out = _new_like(stream, q) if out is None else _dense(out, q.shape, q.dtype, "out")
     ws = _kv8_workspace(cache, q_len, heads, stream)
     _check("tp_mlp_kv8_attention",
            _lib.tp_mlp_kv8_attention(cache, layer, _ptr(q), stride, _ptr(seqs), _ptr(positions), n, q_len, heads,
@@ -612,11 +619,11 @@ def tp_mlp_kv8_attention_partials(cache: Kv8Cache, layer: int, q: torch.Tensor, 
 
     def stat(t, what):
         if t is None:
-            return _new((n, q_len, heads), torch.float32, q.device, stream)
+            return _new(stream, n, q_len, heads, dtype=torch.float32, device=q.device)
         return _dense(t, (n, q_len, heads), torch.float32, what)
 
     maximum, exp_sum = stat(maximum, "maximum"), stat(exp_sum, "exp_sum")
-    weighted = _new(q.shape, q.dtype, q.device, stream) if weighted is None else \
+    weighted = _new_like(stream, q) if weighted is None else \
         _dense(weighted, q.shape, q.dtype, "weighted")
     ws = _kv8_workspace(cache, q_len, heads, stream)
     _check("tp_mlp_kv8_attention_partials",

@@ -112,7 +112,7 @@ class KvCache8:
     def compact(self, new_index: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Returns the new number of every page (-1 for pages that were free)."""
         if new_index is None:
-            new_index = binding._new(self.num_pages, torch.int32, self.device, stream)
+            new_index = binding._new(stream, self.num_pages, dtype=torch.int32, device=self.device)
         binding.tp_mlp_kv8_compact(self._on(), new_index, stream)
         return new_index
 
