@@ -678,7 +678,8 @@ int tp_mlp_kv8_append(const tp_mlp_kv8_cache *cache, int layer, const void *k, c
  *     s_t = scale * q . k_t,   out = sum_t exp(s_t) v_t / sum_t exp(s_t)
  * A query that sees no token gets zeros.  Entries whose sequence number is -1
  * or invalid leave their rows of the output as they were; keys of an invalid
- * page count as unseen.  fp32 softmax and accumulation.
+ * page count as unseen.  fp32 softmax and accumulation; on pages whose value
+ * scale is above 2^90, weights below 2^-132 * scale of a row's largest are lost.
  *   q          device, n * q_len rows of heads x head_dim elements of `dtype`,
  *              a row every row_stride elements (16-byte row starts)
  *   out        device, n x q_len x heads x head_dim of `dtype`, dense

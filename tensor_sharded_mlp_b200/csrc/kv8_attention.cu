@@ -39,7 +39,10 @@
 // when a score exceeds it by 2^15 (one vote a step; the sums are rescaled then).
 // Scores, sums and outputs are fp32; the mma's own sum, which cuts what it
 // shifts out, carries bf16 outputs over a warp's share (at most 2^-23 a step of
-// 16 tokens, so 2^-11 at 64 Ki tokens).
+// 16 tokens, so 2^-11 at 64 Ki tokens).  2^(s_t - R) is 2^6 / v_scale at the
+// largest score, so above a v_scale of 2^90 the exp2, which ends at 2^-126, loses
+// weights of 2^-132 v_scale of the largest and less; one that does not took a
+// third longer for 128 rows.
 //
 // Warps whose pieces meet in one segment (entry, KV head, row tile) join them
 // in shared memory; pieces of a segment that CTAs share go to the workspace (at
@@ -350,8 +353,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                     m = fmaxf(ref[nt][x], m - kLift);
                     const float turn = m == ref[nt][x] ? 1.f : exp2_fast(ref[nt][x] - m);
+                    sum[nt][x] = turn_sum(sum[nt][x], turn, ref[nt][x] - m);
                     ref[nt][x] = m;
-                    sum[nt][x] *= turn;
 #pragma unroll
                     for (int mt = 0; mt < kMt; ++mt) {
                         o[nt][mt][x] *= turn;
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         for (uint32_t m = mine; m; m &= m - 1) ref = fmaxf(ref, stat_of(__ffs(m) - 1)->x);
         for (uint32_t m = mine; m; m &= m - 1) {
             const float4 st = *stat_of(__ffs(m) - 1);
-            l += st.y * (st.x == ref ? 1.f : exp2f(st.x - ref));
+            l += turn_sum(st.y, st.x == ref ? 1.f : exp2f(st.x - ref), st.x - ref);
             tp = fmaxf(tp, st.z);
         }
         float f = own == ref ? 1.f : exp2f(own - ref);

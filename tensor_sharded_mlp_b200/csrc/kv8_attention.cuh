@@ -126,6 +126,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A sum of weights brought from its reference to one that is `d` <= 0 away; turn = 2^d.  Pages of zeros (the smallest scale)
+// beside pages of large values put references more than 126 apart, and then the sum at the lower one is as much larger.
+__device__ __forceinline__ float turn_sum(float sum, float turn, float d) {
+    const float half = exp2_fast(0.5f * d);
+    return turn >= FLT_MIN ? sum * turn : sum * half * half;
+}
 // Bytes of w that are e4m3 NaN, as 0xff each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
@@ -317,9 +323,9 @@ __global__ void __launch_bounds__(kJoinThreads)
         const float4 stat = *reinterpret_cast<const float4 *>(pc + kRows * D + in_tile * 4);
         const float m = fmaxf(ref, stat.x);
         const float f0 = ref == m ? 1.f : exp2f(ref - m), f1 = stat.x == m ? 1.f : exp2f(stat.x - m);
+        sum = turn_sum(sum, f0, ref - m) + turn_sum(stat.y, f1, stat.x - m);
         ref = m;
         top = fmaxf(top, stat.z);
-        sum = sum * f0 + stat.y * f1;
 #pragma unroll
         for (int x = 0; x < kCols; ++x)
             if (D != 64 || lane < 16) {
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     for (int p = 0; p < kJoinWarps; ++p) {
         const float4 stat = part_stat[my_row][p];
         const float f = stat.x == m ? 1.f : exp2f(stat.x - m);
-        sum += stat.y * f;
+        sum += turn_sum(stat.y, f, stat.x - m);
 #pragma unroll
         for (int x = 0; x < kCols; ++x) {
             const float4 y = part[my_row][p][lane + 32 * x];

@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
                     weights();
                     if (__any_sync(0xffffffffu, m > ref + kSlack)) {
                         const float up = fmaxf(ref, m - kLift), turn = up == ref ? 1.f : exp2_fast(ref - up);
+                        sum = turn_sum(sum, turn, ref - up);
                         ref = up;
-                        sum *= turn;
                         if (w.t > w.t0) {
                             if (!(ok = outputs_done())) break;
                             tc::tc_fence_after();
