@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                     float x = (sc[y][nt][k] + sc2[y][nt][k]) * (fac[nt][k & 1] * kscale[y]);
                     if (masked && s * kStep + g + 8 * (k >> 1) >= limit[nt][k & 1]) x = -INFINITY;
                     sc[y][nt][k] = x;
-                    rise |= x + vlog[y] > ref[nt][k & 1] + kSlack;
+                    rise |= x - ref[nt][k & 1] > kSlack - vlog[y];   // (a difference: exact however large the scores)
                     top[nt][k & 1] = fmaxf(top[nt][k & 1], x);
                 }
         }
@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     float m = -INFINITY;
 #pragma unroll
-                    for (int y = 0; y < kUnits; ++y) m = fmaxf(m, fmaxf(sc[y][nt][x], sc[y][nt][x + 2]) + vlog[y]);
+                    for (int y = 0; y < kUnits; ++y) m = fmaxf(m, fmaxf(sc[y][nt][x], sc[y][nt][x + 2]) + (vlog[y] - kLift));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    m = fmaxf(ref[nt][x], m - kLift);
+                    m = fmaxf(ref[nt][x], m);
                     const float turn = m == ref[nt][x] ? 1.f : exp2_fast(ref[nt][x] - m);
                     sum[nt][x] = turn_sum(sum[nt][x], turn, ref[nt][x] - m);
                     ref[nt][x] = m;

@@ -369,8 +369,9 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
                         }
                         return (float)max((int)((__float_as_uint(ks.y) & 0x7fffffffu) >> 23) - 126, kLeastLog);
                     };
-                    float m = -INFINITY;
-                    if (w.t == w.t0) {     // the first tile sets the reference
+                    // the reference that this tile's scores ask for
+                    auto tile_ref = [&]() {
+                        float m = -INFINITY;
 #pragma unroll 2
                         for (int gr = 0; gr < kTok / 16; ++gr) {
                             float s[16];
@@ -380,14 +381,15 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
                             float x = s[0];
 #pragma unroll
                             for (int k = 1; k < 16; ++k) x = fmaxf(x, s[k]);
-                            m = fmaxf(m, x + vlog);
+                            m = fmaxf(m, x + (vlog - kLift));
                         }
-                        ref = fmaxf(ref, m - kLift);
-                    }
-                    float part;
+                        return fmaxf(ref, m);
+                    };
+                    if (w.t == w.t0) ref = tile_ref();
+                    float part, above;   // above: how far a score lies above the reference (a difference: exact however large)
                     auto weights = [&]() {
                         part = 0.f;
-                        m = -INFINITY;
+                        above = -INFINITY;
 #pragma unroll 2
                         for (int gr = 0; gr < kTok / 16; ++gr) {
                             float s[16];
@@ -408,13 +410,13 @@ __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
                             }
                             part += l0 + l1;
                             top = fmaxf(top, x);
-                            m = fmaxf(m, x + vlog);
+                            above = fmaxf(above, (x - ref) + vlog);
                             tmem_st8(lanes + C::kWeights + slot * (kTok / 2) + 8 * gr, h);
                         }
                     };
                     weights();
-                    if (__any_sync(0xffffffffu, m > ref + kSlack)) {
-                        const float up = fmaxf(ref, m - kLift), turn = up == ref ? 1.f : exp2_fast(ref - up);
+                    if (__any_sync(0xffffffffu, above > kSlack)) {
+                        const float up = tile_ref(), turn = up == ref ? 1.f : exp2_fast(ref - up);
                         sum = turn_sum(sum, turn, ref - up);
                         ref = up;
                         if (w.t > w.t0) {

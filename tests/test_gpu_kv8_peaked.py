@@ -6,6 +6,8 @@ small, but its weight still has 11 bits (bf16 results: fp16) or 22 (fp32: two pa
 at a row's largest score (it lies in [2^6, 2^15)) and fp16 is full down to 2^-14, so that holds down to 2^-20 of the
 largest weight; below it an absolute 2^-25 takes over (fp32: 2^-37, the lower part is held 2^12 times as large), that is
 2^-31 (2^-43) of the largest for each token."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
@@ -129,3 +131,29 @@ def test_a_query_element_far_above_the_others(dtype, head_dim, q_len, heads, siz
     q = query(r, 2, q_len, heads, head_dim, dtype)
     q[..., 3] = size
     check(c, on_gpu(c), q, [0, 1])
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype,head_dim,q_len,heads", SHAPES)
+def test_values_of_one_under_scores_of_millions(dtype, head_dim, q_len, heads, sign):
+    """fp32 scores of that size lie up to 8 apart, but whatever the weights, their mean of ones is one: no weight may leave
+    fp16's range, and each must count the same in both sums (11 or 22 bits, and a sum's own 2^-23 a step)."""
+    r = np.random.default_rng(head_dim)
+    n = 700
+    c = kv8.new_cache(1, 11, 1, 64, head_dim, 1, 11)
+    c["refcount"][:], c["table"][0], c["lengths"][0] = 1, np.arange(11), n
+    c["v"][:] = kv8.encode(1.0)
+    c["k"][0, :, 0, :, 0] = kv8.encode(15.0)
+    c["k"][0, :, 0, :, 1] = kv8.encode(np.sort(r.choice(kv8._POS[kv8._POS <= 30], 704)).reshape(11, 64))     # rising
+    cache = on_gpu(c)
+    times = 300 if head_dim == 256 else 600                             # (a warp or a CTA has the sequence for itself)
+    seqs = ints([0] * times)
+    q = torch.zeros(times, q_len, heads, head_dim, device="cuda", dtype=TORCH[dtype])
+    for log, binade in itertools.product((10, 16, 19, 20, 21, 22), (-9, -6, -4, -1, 0, 1, 2, 3, 4, 5, 6, 8, 11, 12, 13, 14)):
+        scale = float(np.float32(1.99)) * 2.0 ** binade                 # up to 15 * 2^22 nats, 2^26.5 base-2 logs
+        cache.v_scale.fill_(scale)
+        q[..., 0], q[..., 1] = sign * 2.0 ** log, 1.0
+        out = cache.attention(0, q, seqs, scale=1.0).double() / scale
+        err = float((out - 1).abs().nan_to_num(1e9).max())
+        bound = (2.0 ** -8 + 2.0 ** -11 if dtype == "bf16" else 2.0 ** -24 + 2.0 ** -22) + 2 * (n / 16 + 8) * 2.0 ** -23 + 2.0 ** -21
+        assert err <= bound, (log, binade, err, bound)
