@@ -18,9 +18,9 @@
 // is: a warp takes a unit, and the rows are loaded beside the page's refcount.
 //
 // Measured (B200; bf16, 8 KV heads of 128, pages of 64): 8 prompts of 500 to
-// 8001 tokens, 191 MB, 36.9 us = 5.2 TB/s, 0.79 of the copy rate: about 5 us of
+// 8001 tokens, 191 MB, 37.0 us = 5.2 TB/s, 0.79 of the copy rate: about 5 us of
 // dependent loads before the first row, then issue slots (58 % busy) and the
-// barrier of each unit's maximum; 256 single tokens 6.2 us.  Tried: two units'
+// barrier of each unit's maximum; 256 single tokens 6.4 us.  Tried: two units'
 // rows in registers (120 of them, 2 CTAs an SM) 53.6 us; prefetching the next
 // unit into L2 41.6 against 39.5; 5 CTAs an SM 54.8.
 #include "common.cuh"

@@ -53,11 +53,15 @@
 // just their outputs.
 //
 // Measured (B200; 64 heads on 8 KV heads of 128, bf16): 32 sequences of 20001
-// to 36001 tokens, 1.84 GB, 281-288 us = 6.4-6.5 TB/s, 0.98-1.00 of the copy
+// to 36001 tokens, 1.84 GB, 285-290 us = 6.3-6.5 TB/s, 0.97-0.99 of the copy
 // rate (295-310 us in thousands of calls in a row, under the power cap); 32 of
-// 300 to 6000 tokens 43.9 us, of which a kernel that loads the same and computes
+// 300 to 6000 tokens 44.7 us, of which a kernel that loads the same and computes
 // nothing takes 42.5: lists, first loads, joins and the second launch are some
-// 10 us; one sequence of 4099 tokens 12.0 us.  What was tried beside this form:
+// 10 us; one sequence of 4099 tokens 12.2 us.  fp32, 16 sequences of 4000 tokens,
+// 8 / 16 / 32 / 64 / 128 rows a KV head: 29 / 37 / 62 / 101 / 186 us for head_dim 64,
+// 37 / 57 / 94 / 172 / 321 for 128, 59 / 98 / 178 / 340 / 680-750 for 256 (21 us of bytes at
+// 128): every row tile reads and converts the history again; of it the lower parts'
+// scaling is 3-5 %.  What was tried beside this form:
 //   12 or 16 warps a CTA: more pieces to join, 1.04-1.1 times as long;
 //   one step at a time instead of two: 332 against 309 us under the power cap;
 //   the score product on the 8-bit mma with the query as two e4m3 parts: 279

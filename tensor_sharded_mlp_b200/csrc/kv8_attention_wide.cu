@@ -23,9 +23,9 @@
 //
 // Measured (B200, bf16, 8 KV heads, 16 sequences of 4000 tokens; kv8_attention.cu's kernel -> this one, us):
 //   rows            72            128            256           1024
-//   head_dim 64   103 -> 75     132 -> 80      244 -> 142     914 -> 507
-//   head_dim 128  144 -> 92     220 -> 98      429 -> 174    1652 -> 623
-//   head_dim 256  294 -> 155    606 -> 165    1243 -> 297    4912 -> 1068
+//   head_dim 64   103 -> 76     132 -> 82      244 -> 144     914 -> 515
+//   head_dim 128  144 -> 92     220 -> 98      429 -> 173    1652 -> 617
+//   head_dim 256  294 -> 155    606 -> 166    1243 -> 300    4912 -> 1082
 // What bounds it: a tile's way through the two places of keys and values (some 4300 cycles for 128 tokens of 128 columns:
 // codes to operands 1700, scores 1000, softmax 3300, outputs 1000, each behind a barrier; two tiles are on it at a time).
 // The tensor pipe is busy 19 % of the time.  Tried beside this form (64 rows of head_dim 128, 95 us): weights through shared
@@ -589,7 +589,10 @@ cudaError_t launch_either(const Kv8 &c, const Kv8Query &a, void *ws, int num_sms
 //                 64                119 / 91          69 / 65      44 / 58     16 / 18      18 / 24
 //   head_dim 64,  33-64 rows         76 / 73-74       49-50 / 50   38 / 43     18 / 15      22 / 21
 // The lengths are the device's to know.  The host has a bound of the tokens that a call can see, and up to 64 rows this
-// kernel is taken only where those of all KV heads may be 2^18 (16 x 4000 x 8 are 2^19, 32 x 1000 x 8 are 2^18).
+// kernel is taken only where those of all KV heads may be 2^18 (16 x 4000 x 8 are 2^19, 32 x 1000 x 8 are 2^18).  Above 64
+// rows it always is, for the table at the head of this file; what that costs short histories (head_dim 64, 128, 256): one
+// sequence of 4000 tokens, 72 rows 22 -> 22, 20 -> 25, 38 -> 40, 128 rows 24 -> 25, 25 -> 28, 45 -> 48; 8 of 100 to 300 tokens,
+// 128 rows 21 -> 18, 20 -> 22, 29 -> 36.
 namespace {
 constexpr int kAlwaysWide = 64;
 int wide_rows_from(int head_dim) { return head_dim == 256 ? 32 : head_dim == 128 ? 48 : kAlwaysWide; }

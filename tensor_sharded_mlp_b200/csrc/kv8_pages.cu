@@ -15,7 +15,12 @@
 // written), with a saved map put back and a truncation before it, 128 us, 110 of
 // them the copy = 6.35 TB/s, 0.97 of the copy rate; the same on a pool of 73
 // pages 12.8 us; putting back, a fork and a reserve that copies 32 pages of 4
-// layers 20.8 us.
+// layers 20.8 us.  A reserve of one token each, nothing to copy: 1 / 32 / 256 / 1024
+// sequences 7.4 / 8.1 / 9.9 / 24 us (pool of 8192 pages; 65536: 8.2 / 9.1 / 11 / 25).
+// Each entry's thread looks through the list in front of it for a repeat, and where
+// pages are shared through the whole list for their holders: half the list's
+// sequences sharing their last page with the other half, 32 / 256 / 1024 entries take
+// 12 / 17 / 67 us with the copies.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -553,7 +558,7 @@ unsigned map_ctas(const Kv8 &c) { return c.num_pages <= kMapOneCta ? 1 : kMapCta
 
 unsigned copy_grid(const Kv8 &c, long long pairs, int num_sms) {
     const long long tiles = (c.page_bytes() / 16 + kTile - 1) / kTile * c.layers * 2 * pairs;
-    const long long most = 8LL * num_sms;   // 8 CTAs of 256 threads fill an SM
+    const long long most = 8LL * num_sms;   // (3 CTAs of 72 registers a thread are resident: 2.7 rounds)
     return (unsigned)(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }
 
