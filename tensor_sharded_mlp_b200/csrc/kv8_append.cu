@@ -186,7 +186,7 @@ __device__ __forceinline__ Slot find_slot(const Kv8 &c, Lists l, long long slot,
         row0 = i * count;
     }
     const int seq = l.seq[i];
-    if (j < 0 || count == 0 || seq == -1) return out;
+    if (j < 0 || seq == -1) return out;
     if ((unsigned)seq >= (unsigned)c.max_seqs || kv8_repeats(l.listed ? l.seq : nullptr, i, seq)) {
         if (teller && j == 0) kv8_flag(c, TP_MLP_KV8_BAD_SEQUENCE);
         return out;
@@ -196,6 +196,7 @@ __device__ __forceinline__ Slot find_slot(const Kv8 &c, Lists l, long long slot,
         if (teller && j == 0) kv8_flag(c, TP_MLP_KV8_BAD_LENGTH);
         return out;
     }
+    if (count == 0) return out;
     const long long nth = (start >> c.page_shift) + j;
     if (nth > (len - 1) >> c.page_shift) return out;
     const int page = c.table[(long long)seq * c.max_pages + nth];

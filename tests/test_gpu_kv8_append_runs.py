@@ -141,3 +141,20 @@ def test_row_bounds_out_of_order_in_long_lists(dtype):
         off = cu.copy()
         off[at] += by
         put(c, cache, 0, k, v, list(range(n)), off)
+
+
+@pytest.mark.parametrize("each", [1, 40])
+def test_entries_without_rows_are_checked_too(each):
+    """A wrong sequence number or length is flagged though its entry has nothing to write."""
+    r = np.random.default_rng(34)
+    c = filled(r, [50, 60, 70, 17], 1, 3, 16, 64)
+    cache = on_gpu(c)
+    k, v = rows(r, 2 * each, 3, 64, "bf16")
+    put(c, cache, 0, k, v, [0, 1, 0], [0, each, 2 * each, 2 * each])
+    put(c, cache, 0, k, v, [4, 1, 0], [0, 0, each, 2 * each])
+    put(c, cache, 0, k, v, [0, -9, 1], [0, each, each, 2 * each])
+    put(c, cache, 0, k, v, [0, 3, -1, 1], [0, each, each, each, 2 * each])
+    c["lengths"][3] = 10000
+    cache.lengths[3] = 10000
+    put(c, cache, 0, k, v, [0, 3, 1], [0, each, each, 2 * each])
+    assert kv8.append(c, 0, np.zeros((0, 3, 64)), np.zeros((0, 3, 64)), [3], [0, 0]) == kv8.BAD_LENGTH
