@@ -658,9 +658,9 @@ int tp_mlp_kv8_compact(const tp_mlp_kv8_cache *cache, int *new_index, void *work
  *              a row every row_stride elements (>= kv_heads * head_dim; a row
  *              starts on a 16-byte boundary)
  *   seqs       device, n ints (NULL: sequence i); each sequence once
- *   cu_tokens  device, n + 1 ints, ascending from 0, or NULL.  An entry whose two bounds are below an earlier bound
- *              or 0, in falling order or beyond `tokens` is left out and flagged (TP_MLP_KV8_BAD_LENGTH); rows that
- *              no entry has (those behind cu_tokens[n] of a padded input) are not looked at
+ *   cu_tokens  device, n + 1 ints, ascending from 0, or NULL.  An entry that begins below 0 or below an earlier bound,
+ *              ends before it begins or ends beyond `tokens` is left out and flagged (TP_MLP_KV8_BAD_LENGTH); rows
+ *              that no entry has (those behind cu_tokens[n] of a padded input) are not looked at
  * n <= TP_MLP_KV8_MAX_LIST, tokens <= 4194304; without cu_tokens, tokens % n
  * == 0 (TP_MLP_ERR_SHAPE).  tokens == 0 or n == 0 is a no-op.
  */
@@ -678,8 +678,9 @@ int tp_mlp_kv8_append(const tp_mlp_kv8_cache *cache, int layer, const void *k, c
  *     s_t = scale * q . k_t,   out = sum_t exp(s_t) v_t / sum_t exp(s_t)
  * A query that sees no token gets zeros.  Entries whose sequence number is -1
  * or invalid leave their rows of the output as they were; keys of an invalid
- * page count as unseen.  fp32 softmax and accumulation; on pages whose value
- * scale is above 2^90, weights below 2^-132 * scale of a row's largest are lost.
+ * page count as unseen.  fp32 softmax and accumulation; where the largest value
+ * scale of a row's pages is above 2^90, weights below 2^-132 * scale of the row's
+ * largest are lost, where it is below 2^-81, those below 2^-112 / scale.
  *   q          device, n * q_len rows of heads x head_dim elements of `dtype`,
  *              a row every row_stride elements (16-byte row starts)
  *   out        device, n x q_len x heads x head_dim of `dtype`, dense

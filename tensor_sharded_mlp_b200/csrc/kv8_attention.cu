@@ -42,7 +42,8 @@
 // 16 tokens, so 2^-11 at 64 Ki tokens).  2^(s_t - R) is 2^6 / v_scale at the
 // largest score, so above a v_scale of 2^90 the exp2, which ends at 2^-126, loses
 // weights of 2^-132 v_scale of the largest and less; one that does not took a
-// third longer for 128 rows.
+// third longer for 128 rows.  Below a v_scale of 2^-81 (kLeastLog) the largest
+// weight is lower than 2^6, and what counts ends at 2^-112 / v_scale of it.
 //
 // Warps whose pieces meet in one segment (entry, KV head, row tile) join them
 // in shared memory; pieces of a segment that CTAs share go to the workspace (at
